@@ -15,7 +15,9 @@
 #include "fa.h"
 #include "fa_common.cuh"
 #include "fa_decode_sm100.cuh"
+#include "fa_pages_sm100.cuh"
 #include "fa_prefill_sm100.cuh"
+#include "fa_rope_sm100.cuh"
 
 namespace {
 
@@ -509,6 +511,169 @@ int decode_general(const void *q, const CacheDesc &c, const int *seqlens, void *
 
 }  // namespace
 
+// ---------------------------------------------- rotary positions and cache filling
+
+namespace {
+
+// Where fa_cache_append and fa_rope_append write.
+struct PageDest {
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    const int *block_table, *cu_seqlens, *seqlens;
+    int B, num_pages, page_size, max_pages;
+};
+
+bool stride_ok(long long stride, int heads, int d, int elem)
+{
+    return heads == 0 || (stride >= (long long)heads * d && (stride * elem) % 16 == 0);
+}
+
+template <int D, typename T, bool PAGES, bool FP8>
+void launch_rope(const fa::RopeParams &p, bool rot, bool vec, int grid, cudaStream_t st)
+{
+    constexpr int threads = 32 * fa::rope::kWarps;
+    if constexpr (PAGES) {
+        if (!rot) {
+            fa::fa_rope_kernel<D, T, PAGES, FP8, false, true><<<grid, threads, 0, st>>>(p);
+            return;
+        }
+    }
+    if (vec) fa::fa_rope_kernel<D, T, PAGES, FP8, true, true><<<grid, threads, 0, st>>>(p);
+    else fa::fa_rope_any_kernel<D, T, PAGES, FP8><<<grid, threads, 0, st>>>(p);
+}
+
+// Validation and launch shared by fa_rope (pages null), fa_rope_append and fa_cache_append
+// (inv_freq null: nothing is rotated).
+int rope_general(fa::RopeParams &p, const PageDest *pages, int d, int dtype, void *stream)
+{
+    const bool rot = p.inv_freq != nullptr;
+    if (dtype != FA_BF16 && dtype != FA_F32) return fail(FA_ERR_INVALID, "unknown dtype %d", dtype);
+    if (p.T <= 0 || p.Hq < 0 || p.Hkv < 0 || p.Hq + p.Hkv <= 0 || d <= 0)
+        return fail(FA_ERR_INVALID, "sizes must be positive (T=%d Hq=%d Hkv=%d d=%d)", p.T, p.Hq, p.Hkv, d);
+    if ((p.Hq && (!p.q || !p.q_out)) || (p.Hkv && !p.k) || (!pages && p.Hkv && !p.k_out) || (pages && !p.v))
+        return fail(FA_ERR_INVALID, "null pointer argument");
+    if (rot && !p.positions) return fail(FA_ERR_INVALID, "null positions");
+    if (rot && (p.F <= 0 || p.F > d / 2)) return fail(FA_ERR_INVALID, "F (%d) must lie in [1, d / 2]", p.F);
+    if (rot && p.A <= 0) return fail(FA_ERR_INVALID, "A (%d) must be positive", p.A);
+    if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", d);
+    const int es = dtype == FA_F32 ? 4 : 2;
+    if (!stride_ok(p.q_s, p.Hq, d, es) || !stride_ok(p.qo_s, p.Hq, d, es) || !stride_ok(p.k_s, p.Hkv, d, es) ||
+        (!pages && !stride_ok(p.ko_s, p.Hkv, d, es)) || (pages && !stride_ok(p.v_s, p.Hkv, d, es)))
+        return fail(FA_ERR_UNSUPPORTED, "a token stride must hold the heads and be a multiple of 16 bytes");
+    if (!aligned16(p.q) || !aligned16(p.q_out) || !aligned16(p.k) || !aligned16(p.k_out) || !aligned16(p.v))
+        return fail(FA_ERR_UNSUPPORTED, "q, k, v and the outputs must be 16-byte aligned");
+    bool fp8 = false;
+    if (pages) {
+        if (!pages->k || !pages->v || !pages->block_table || !pages->cu_seqlens || !pages->seqlens)
+            return fail(FA_ERR_INVALID, "null pointer argument");
+        if ((pages->k_scale == nullptr) != (pages->v_scale == nullptr))
+            return fail(FA_ERR_INVALID, "give both FP8 scale pointers or neither");
+        if (p.Hkv <= 0 || pages->B <= 0 || pages->num_pages <= 0 || pages->page_size <= 0 || pages->max_pages <= 0)
+            return fail(FA_ERR_INVALID, "sizes must be positive (Hkv=%d B=%d num_pages=%d page_size=%d max_pages=%d)",
+                        p.Hkv, pages->B, pages->num_pages, pages->page_size, pages->max_pages);
+        fp8 = pages->k_scale != nullptr;
+        if (fp8 && d != 128) return fail(FA_ERR_UNSUPPORTED, "FP8 caches need d = 128 (got %d)", d);
+        if (pages->page_size % 16 != 0)
+            return fail(FA_ERR_UNSUPPORTED, "page_size %d is not a multiple of 16", pages->page_size);
+        if (!aligned16(pages->k) || !aligned16(pages->v))
+            return fail(FA_ERR_UNSUPPORTED, "the page pools must be 16-byte aligned");
+        p.kpages = pages->k;
+        p.vpages = pages->v;
+        p.k_scale = pages->k_scale;
+        p.v_scale = pages->v_scale;
+        p.block_table = pages->block_table;
+        p.cu_seqlens = pages->cu_seqlens;
+        p.seqlens = pages->seqlens;
+        p.B = pages->B;
+        p.num_pages = pages->num_pages;
+        p.page_size = pages->page_size;
+        p.max_pages = pages->max_pages;
+    }
+    int dev, rc;
+    DeviceInfo *info;
+    if ((rc = current_device(&dev, &info)) != FA_OK) return rc;
+
+    // A warp takes a whole token when there are tokens enough to fill the GPU; with fewer, a
+    // token's rows are shared out, at least one load of rows per warp.
+    const int chunks = d * es / 16, rows_at_once = 64 / chunks;
+    const int rows = p.Hq + p.Hkv + (pages ? p.Hkv : 0);
+    const int max_split = (rows + rows_at_once - 1) / rows_at_once;
+    const int warps = info->num_sms * 32;
+    p.split = warps / p.T;
+    if (p.split > max_split) p.split = max_split;
+    if (p.split < 1) p.split = 1;
+    const long long ctas = ((long long)p.T * p.split + fa::rope::kWarps - 1) / fa::rope::kWarps;
+    const int max_ctas = info->num_sms * 8;
+    const int grid = ctas < max_ctas ? (int)ctas : max_ctas;
+    const int per = 16 / es;  // elements per 16-byte chunk
+    const bool vec = p.interleaved ? (2 * p.F) % per == 0 : p.F % per == 0;
+
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pages) {
+        if (fp8) launch_rope<128, __nv_bfloat16, true, true>(p, rot, vec, grid, st);
+        else if (d == 128) launch_rope<128, __nv_bfloat16, true, false>(p, rot, vec, grid, st);
+        else launch_rope<64, __nv_bfloat16, true, false>(p, rot, vec, grid, st);
+    } else if (dtype == FA_F32) {
+        if (d == 128) launch_rope<128, float, false, false>(p, true, vec, grid, st);
+        else launch_rope<64, float, false, false>(p, true, vec, grid, st);
+    } else {
+        if (d == 128) launch_rope<128, __nv_bfloat16, false, false>(p, true, vec, grid, st);
+        else launch_rope<64, __nv_bfloat16, false, false>(p, true, vec, grid, st);
+    }
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(FA_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ page management
+
+namespace {
+
+int make_tables(fa::PageTables *t, int *block_table, int *seqlens, int *refcount, int S, int max_pages,
+                int num_pages, int page_size, DeviceInfo **info)
+{
+    if (!block_table || !seqlens || !refcount) return fail(FA_ERR_INVALID, "null pointer argument");
+    if (S <= 0 || max_pages <= 0 || num_pages <= 0 || page_size <= 0)
+        return fail(FA_ERR_INVALID, "sizes must be positive (S=%d max_pages=%d num_pages=%d page_size=%d)", S,
+                    max_pages, num_pages, page_size);
+    if (page_size % 16 != 0) return fail(FA_ERR_UNSUPPORTED, "page_size %d is not a multiple of 16", page_size);
+    if ((long long)page_size * max_pages > 0x7fffffffLL - page_size || num_pages >= (1 << 21) - 1 || S > (1 << 20))
+        return fail(FA_ERR_UNSUPPORTED, "problem too large");
+    *t = fa::PageTables{block_table, seqlens, refcount, S, max_pages, num_pages, page_size};
+    int dev;
+    return current_device(&dev, info);
+}
+
+size_t reserve_ws_bytes(int S, int num_pages)
+{
+    if (S <= 0 || num_pages <= 0) return 0;
+    return align256((size_t)S * 4) + align256((size_t)num_pages * 4);
+}
+
+size_t compact_ws_bytes(int num_pages)
+{
+    if (num_pages <= 0) return 0;
+    return 256 + 2 * align256((size_t)num_pages * 4);
+}
+
+int check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (!ws || have < need) return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, have);
+    if (!aligned16(ws)) return fail(FA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    return FA_OK;
+}
+
+int launched(const char *what)
+{
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(FA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    return ok();
+}
+
+}  // namespace
+
 extern "C" {
 
 int fa_fwd(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq,
@@ -733,6 +898,157 @@ int fa_decode_noalloc(const void *q, const void *kcache, const void *vcache, con
                           (size_t)FA_NOALLOC_SCRATCH_BYTES, stream);
 }
 
+// ---------------------------------------------- rotary positions and cache filling
+
+int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *positions, const float *inv_freq,
+            const int *axes, int T, int Hq, int Hkv, int d, int F, int A, long long q_stride, long long k_stride,
+            long long q_out_stride, long long k_out_stride, int dtype, int interleaved, int inverse, void *stream)
+{
+    if (!inv_freq) return fail(FA_ERR_INVALID, "null pointer argument");
+    fa::RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q, p.k = k, p.q_out = q_out, p.k_out = k_out;
+    p.q_s = q_stride, p.k_s = k_stride, p.qo_s = q_out_stride, p.ko_s = k_out_stride;
+    p.positions = positions, p.inv_freq = inv_freq, p.axes = axes;
+    p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.F = F, p.A = A;
+    p.interleaved = interleaved ? 1 : 0;
+    p.inverse = inverse ? 1 : 0;
+    return rope_general(p, nullptr, d, dtype, stream);
+}
+
+int fa_rope_append(const void *q, const void *k, const void *v, void *q_out, const int *positions,
+                   const float *inv_freq, const int *axes, void *kpages, void *vpages, const float *k_scale,
+                   const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens, int T,
+                   int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages, int d, int F, int A,
+                   long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
+                   int interleaved, void *stream)
+{
+    if (!inv_freq) return fail(FA_ERR_INVALID, "null pointer argument");
+    fa::RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = q, p.k = k, p.v = v, p.q_out = q_out;
+    p.q_s = q_stride, p.k_s = k_stride, p.v_s = v_stride, p.qo_s = q_out_stride;
+    p.positions = positions, p.inv_freq = inv_freq, p.axes = axes;
+    p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.F = F, p.A = A;
+    p.interleaved = interleaved ? 1 : 0;
+    const PageDest dest{kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, B, num_pages, page_size, max_pages};
+    return rope_general(p, &dest, d, FA_BF16, stream);
+}
+
+int fa_cache_append(const void *k, const void *v, void *kpages, void *vpages, const float *k_scale,
+                    const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens, int T,
+                    int B, int Hkv, int num_pages, int page_size, int max_pages, int d, long long k_stride,
+                    long long v_stride, void *stream)
+{
+    fa::RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.k = k, p.v = v, p.k_s = k_stride, p.v_s = v_stride;
+    p.T = T, p.Hkv = Hkv;
+    const PageDest dest{kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, B, num_pages, page_size, max_pages};
+    return rope_general(p, &dest, d, FA_BF16, stream);
+}
+
+// ------------------------------------------------------------------ page management
+
+int fa_pages_fork(int *block_table, int *seqlens, int *refcount, const int *src, const int *dst, const int *lengths,
+                  int n, int S, int max_pages, int num_pages, int page_size, void *stream)
+{
+    if (!src || !dst) return fail(FA_ERR_INVALID, "null pointer argument");
+    if (n <= 0) return fail(FA_ERR_INVALID, "n must be positive (%d)", n);
+    if (n > 65535) return fail(FA_ERR_UNSUPPORTED, "at most 65535 pairs in one call (%d)", n);
+    fa::ForkParams p;
+    DeviceInfo *info;
+    const int rc = make_tables(&p.t, block_table, seqlens, refcount, S, max_pages, num_pages, page_size, &info);
+    if (rc != FA_OK) return rc;
+    p.src = src, p.dst = dst, p.lengths = lengths, p.n = n;
+    fa::fa_pages_fork_kernel<<<n, fa::pages::kSlotThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("fork");
+}
+
+int fa_pages_free(int *block_table, int *seqlens, int *refcount, const int *slots, const int *keep, int n, int S,
+                  int max_pages, int num_pages, int page_size, void *stream)
+{
+    if (!slots) return fail(FA_ERR_INVALID, "null pointer argument");
+    if (n <= 0) return fail(FA_ERR_INVALID, "n must be positive (%d)", n);
+    if (n > 65535) return fail(FA_ERR_UNSUPPORTED, "at most 65535 slots in one call (%d)", n);
+    fa::FreeParams p;
+    DeviceInfo *info;
+    const int rc = make_tables(&p.t, block_table, seqlens, refcount, S, max_pages, num_pages, page_size, &info);
+    if (rc != FA_OK) return rc;
+    p.slots = slots, p.keep = keep, p.n = n;
+    fa::fa_pages_free_kernel<<<n, fa::pages::kSlotThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("free");
+}
+
+size_t fa_pages_reserve_workspace_size(int S, int num_pages) { return reserve_ws_bytes(S, num_pages); }
+
+int fa_pages_reserve(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int S, int max_pages,
+                     int num_pages, int page_size, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!add || !copies) return fail(FA_ERR_INVALID, "null pointer argument");
+    fa::ReserveParams p;
+    DeviceInfo *info;
+    int rc = make_tables(&p.t, block_table, seqlens, refcount, S, max_pages, num_pages, page_size, &info);
+    if (rc != FA_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, reserve_ws_bytes(S, num_pages))) != FA_OK) return rc;
+    p.add = add, p.copies = copies;
+    p.first = static_cast<int *>(workspace);
+    p.free_ids = reinterpret_cast<int *>(static_cast<char *>(workspace) + align256((size_t)S * 4));
+    fa::fa_pages_reserve_kernel<<<1, fa::pages::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("reserve");
+}
+
+size_t fa_pages_compact_workspace_size(int num_pages) { return compact_ws_bytes(num_pages); }
+
+int fa_pages_compact(int *block_table, int *seqlens, int *refcount, int *copies, int S, int max_pages, int num_pages,
+                     int page_size, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!copies && num_pages > 1) return fail(FA_ERR_INVALID, "null pointer argument");
+    fa::CompactParams p;
+    DeviceInfo *info;
+    int rc = make_tables(&p.t, block_table, seqlens, refcount, S, max_pages, num_pages, page_size, &info);
+    if (rc != FA_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, compact_ws_bytes(num_pages))) != FA_OK) return rc;
+    p.copies = copies;
+    p.n_live = static_cast<int *>(workspace);
+    p.map = reinterpret_cast<int *>(static_cast<char *>(workspace) + 256);
+    p.holes = reinterpret_cast<int *>(static_cast<char *>(workspace) + 256 + align256((size_t)num_pages * 4));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    fa::fa_pages_compact_kernel<<<1, fa::pages::kPlanThreads, 0, st>>>(p);
+    if ((rc = launched("compact")) != FA_OK) return rc;
+    fa::fa_pages_remap_kernel<<<S, fa::pages::kSlotThreads, 0, st>>>(p);
+    return launched("compact");
+}
+
+int fa_pages_copy(void *kpages, void *vpages, const int *copies, int n, int num_pages, long long page_bytes,
+                  void *stream)
+{
+    if (!kpages || !copies) return fail(FA_ERR_INVALID, "null pointer argument");
+    if (n < 0 || num_pages <= 0 || page_bytes <= 0)
+        return fail(FA_ERR_INVALID, "sizes must be positive (n=%d num_pages=%d page_bytes=%lld)", n, num_pages, page_bytes);
+    if (page_bytes % 16 != 0 || page_bytes > (1LL << 46) / num_pages)
+        return fail(FA_ERR_UNSUPPORTED, "a page of %lld bytes is not a multiple of 16, or the pool is too large", page_bytes);
+    if (!aligned16(kpages) || !aligned16(vpages))
+        return fail(FA_ERR_UNSUPPORTED, "the page pools must be 16-byte aligned");
+    int dev, rc;
+    DeviceInfo *info;
+    if ((rc = current_device(&dev, &info)) != FA_OK) return rc;
+    if (n == 0) return ok();
+    fa::PageCopyParams p;
+    p.k = static_cast<uint4 *>(kpages);
+    p.v = static_cast<uint4 *>(vpages);
+    p.copies = copies;
+    p.n = n;
+    p.num_pages = num_pages;
+    p.page_vecs = page_bytes / 16;
+    p.pieces = (int)((page_bytes + fa::pages::kPieceBytes - 1) / fa::pages::kPieceBytes);
+    const long long items = (long long)n * p.pieces * (vpages ? 2 : 1);
+    const int max_ctas = info->num_sms * 8;
+    fa::fa_pages_copy_kernel<<<(int)(items < max_ctas ? items : max_ctas), fa::pages::kCopyThreads, 0,
+                               static_cast<cudaStream_t>(stream)>>>(p);
+    return launched("page copy");
+}
+
 int fa_get_error(void *stream)
 {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
@@ -747,7 +1063,14 @@ int fa_get_error(void *stream)
     if (word & fa::kErrTimeout) return fail(FA_ERR_TIMEOUT, "a kernel pipeline wait exceeded its time limit");
     if (word & fa::kErrSeqlenRange) return fail(FA_ERR_DEVICE_ARG, "seqlens held a value outside [0, Nmax]");
     if (word & fa::kErrPageRange)
-        return fail(FA_ERR_DEVICE_ARG, "the block table held a page outside [0, num_pages)");
+        return fail(FA_ERR_DEVICE_ARG, "the block table or a copy list held a page outside [0, num_pages)");
+    if (word & fa::kErrNoPages)
+        return fail(FA_ERR_NO_PAGES, "the pool has fewer free pages than fa_pages_reserve needs; nothing was changed");
+    if (word & fa::kErrSlot)
+        return fail(FA_ERR_DEVICE_ARG, "page management: a slot, length or refcount was not usable");
+    if (word & fa::kErrCuSeqlens)
+        return fail(FA_ERR_DEVICE_ARG, "cu_seqlens does not ascend within [0, T], or disagrees with seqlens");
+    if (word & fa::kErrAxisRange) return fail(FA_ERR_DEVICE_ARG, "axes held a value outside [0, A)");
     if (word & fa::kErrDebugBounds)
         return fail(FA_ERR_DEBUG_CHECK, "a kernel's global-memory index failed its bounds check (access skipped)");
     return ok();
@@ -766,6 +1089,7 @@ const char *fa_status_str(int status)
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
     case FA_ERR_DEVICE_ARG: return "FA_ERR_DEVICE_ARG";
     case FA_ERR_DEBUG_CHECK: return "FA_ERR_DEBUG_CHECK";
+    case FA_ERR_NO_PAGES: return "FA_ERR_NO_PAGES";
     default: return "FA_ERR_UNKNOWN";
     }
 }

@@ -13,6 +13,10 @@ enum : unsigned int {
     kErrSeqlenRange = 2u,  // a decode length was outside [0, Nmax] and was clamped
     kErrPageRange = 4u,    // a block-table entry was outside [0, num_pages); its keys read as 0
     kErrDebugBounds = 8u,  // debug builds: an address computed by a kernel failed its bounds check
+    kErrCuSeqlens = 16u,   // cu_seqlens not ascending within [0, T], or at odds with seqlens
+    kErrAxisRange = 32u,   // an axis outside [0, A); it was read as axis 0
+    kErrSlot = 64u,        // page management: a slot, length or page of the call was not usable
+    kErrNoPages = 128u,    // fa_pages_reserve: fewer free pages than needed; nothing was changed
 };
 
 // One word per process, in the library's own device memory.

@@ -28,11 +28,12 @@ FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
 FA_ERR_DEVICE_ARG = 6
 FA_ERR_DEBUG_CHECK = 7
+FA_ERR_NO_PAGES = 8
 FA_BF16 = 0
 FA_F32 = 1
 
 # Every symbol include/fa.h declares, with its ctypes signature.
-_P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_P, _I, _F, _Z, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_longlong
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
     "fa_fwd_ex": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _I, _P]),
@@ -48,6 +49,16 @@ SIGNATURES = {
     "fa_decode_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _Z, _P]),
     "fa_decode_paged_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                  _P, _Z, _P]),
+    "fa_rope": (_I, [_P] * 7 + [_I] * 6 + [_L] * 4 + [_I] * 3 + [_P]),
+    "fa_cache_append": (_I, [_P] * 9 + [_I] * 7 + [_L] * 2 + [_P]),
+    "fa_rope_append": (_I, [_P] * 14 + [_I] * 10 + [_L] * 4 + [_I, _P]),
+    "fa_pages_reserve_workspace_size": (_Z, [_I, _I]),
+    "fa_pages_reserve": (_I, [_P] * 5 + [_I] * 4 + [_P, _Z, _P]),
+    "fa_pages_fork": (_I, [_P] * 6 + [_I] * 5 + [_P]),
+    "fa_pages_free": (_I, [_P] * 5 + [_I] * 5 + [_P]),
+    "fa_pages_compact_workspace_size": (_Z, [_I]),
+    "fa_pages_compact": (_I, [_P] * 4 + [_I] * 4 + [_P, _Z, _P]),
+    "fa_pages_copy": (_I, [_P] * 3 + [_I, _I, _L, _P]),
     "fa_get_error": (_I, [_P]),
     "fa_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
     "fa_fwd_selftest_timeout": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P]),
@@ -472,6 +483,311 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
                                         _stream_handle(stream, dev))
     _check(rc)
     return out, lse
+
+
+# ------------------------------------------- rotary positions, cache filling, pages
+#
+# These calls are short (a few microseconds on the device), so their checks are the plain
+# ones below: one pass over each tensor's attributes, and the device is switched only when
+# the tensors are not on the current one.
+
+
+def _tensor(t, name, dtype, ndim, dev=None):
+    """A contiguous CUDA tensor of this type and rank (on `dev`)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != dtype or t.dim() != ndim or not t.is_contiguous():
+        _require(t, name, dtype, ndim)
+    if dev is not None and t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}; found {name} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtypes, dev=None):
+    """A (T, H, d) CUDA tensor whose heads are contiguous; tokens may be strided.  Returns
+    (pointer, token stride in elements)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions (tokens, heads, d), got {t.dim()}")
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and st < H * d):
+        raise ValueError(f"{name} must have contiguous heads (strides (*, d, 1)), got {t.stride()}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"all tensors must be on {dev}; found {name} on {t.device}")
+    return t.data_ptr(), (st if T > 1 else H * d)
+
+
+def _launch(fn, dev, stream, *args):
+    """Call the library with the tensors' device current, on `stream` or its current stream."""
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _stream_handle(stream, dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream_handle(stream, dev))
+    if rc != FA_OK:
+        _check(rc)
+
+
+def _scratch(workspace, need, dev):
+    """(pointer, bytes) of the caller's workspace, or of a new one (kept alive by the third)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.device != dev:
+        raise ValueError(f"all tensors must be on {dev}; found workspace on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _rotation(positions, inv_freq, axes, T, d, dev):
+    """Pointers and sizes of the rotation's tables: positions (T,) or (A, T), inv_freq (F,)."""
+    if isinstance(positions, torch.Tensor) and positions.dim() == 1:
+        positions = positions.unsqueeze(0)
+    pp = _tensor(positions, "positions", torch.int32, 2, dev)
+    pf = _tensor(inv_freq, "inv_freq", torch.float32, 1, dev)
+    A, F = positions.shape[0], inv_freq.shape[0]
+    if positions.shape[1] != T:
+        raise ValueError(f"positions must cover {T} tokens, got {tuple(positions.shape)}")
+    pa = None
+    if axes is not None:
+        pa = _tensor(axes, "axes", torch.int32, 1, dev)
+        if axes.shape[0] != F:
+            raise ValueError("axes and inv_freq must have the same length")
+    elif A != 1:
+        raise ValueError("several position axes need `axes`, the axis of each frequency")
+    return pp, pf, pa, F, A
+
+
+_ROPE_TYPES = (torch.bfloat16, torch.float32)
+_BF16 = (torch.bfloat16,)
+
+
+def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor,
+         axes: Optional[torch.Tensor] = None, interleaved: bool = False, inverse: bool = False,
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions (fa_rope): q (T,Hq,d) and k (T,Hkv,d), bf16 or fp32, either may be None;
+    positions int32 (T,) or (A,T); inv_freq fp32 (F,); axes int32 (F,), the axis of each
+    frequency.  Returns (q_out, k_out), new tensors unless given (q_out=q works in place).
+    Tokens may be strided (slices of a fused projection).  inverse=True is the transposed
+    rotation: with the gradients of the outputs as q and k it returns those of the inputs."""
+    if q is None and k is None:
+        raise ValueError("q and k cannot both be None")
+    first = q if q is not None else k
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    dev, dtype = first.device, first.dtype
+    ptrs, strides, heads, outs = [], [], [], []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            ptrs.append((None, None))
+            strides.append((0, 0))
+            heads.append(0)
+            outs.append(None)
+            continue
+        p, s = _rows(x, name, _ROPE_TYPES, dev)
+        if x.dtype != dtype or x.shape[0] != first.shape[0] or x.shape[2] != first.shape[2]:
+            raise ValueError("q and k must have the same type, tokens and head dim")
+        if out is None:
+            out = torch.empty(x.shape, dtype=dtype, device=dev)
+        po, so = _rows(out, name + "_out", (dtype,), dev)
+        if out.shape != x.shape:
+            raise ValueError(f"{name}_out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        ptrs.append((p, po))
+        strides.append((s, so))
+        heads.append(x.shape[1])
+        outs.append(out)
+    T, d = first.shape[0], first.shape[2]
+    pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, d, dev)
+    if T == 0:
+        return outs[0], outs[1]
+    _launch(load().fa_rope, dev, stream, ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1], pp, pf, pa, T, heads[0],
+            heads[1], d, F, A, strides[0][0], strides[1][0], strides[0][1], strides[1][1],
+            FA_F32 if dtype == torch.float32 else FA_BF16, int(bool(interleaved)), int(bool(inverse)))
+    return outs[0], outs[1]
+
+
+def _destination(k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev):
+    """The checks fa_cache_append and fa_rope_append share: (k, v) rows and the pages' arguments."""
+    pk, sk = _rows(k, "k", _BF16, dev)
+    pv, sv = _rows(v, "v", _BF16, dev)
+    T, Hkv, d = k.shape
+    fp8 = k_scale is not None or v_scale is not None
+    pool = torch.uint8 if fp8 else torch.bfloat16
+    pkp, pvp = _tensor(kpages, "kpages", pool, 4, dev), _tensor(vpages, "vpages", pool, 4, dev)
+    pks = pvs = None
+    if fp8:
+        pks, pvs = _tensor(k_scale, "k_scale", torch.float32, 1, dev), _tensor(v_scale, "v_scale", torch.float32, 1, dev)
+        if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+            raise ValueError("k_scale and v_scale must have Hkv entries")
+    pbt = _tensor(block_table, "block_table", torch.int32, 2, dev)
+    pcu, psl = _tensor(cu_seqlens, "cu_seqlens", torch.int32, 1, dev), _tensor(seqlens, "seqlens", torch.int32, 1, dev)
+    num_pages, H, page_size, dk = kpages.shape
+    B, max_pages = block_table.shape
+    if (v.shape != k.shape or (H, dk) != (Hkv, d) or vpages.shape != kpages.shape or seqlens.shape[0] != B
+            or cu_seqlens.shape[0] != B + 1):
+        raise ValueError("shape mismatch between k, v, the pools, block_table, cu_seqlens and seqlens")
+    return (pk, sk), (pv, sv), (pkp, pvp, pks, pvs, pbt, pcu, psl), (T, B, Hkv, num_pages, page_size, max_pages, d)
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor,
+                 block_table: torch.Tensor, cu_seqlens: torch.Tensor, seqlens: torch.Tensor,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None, stream=None):
+    """Put new tokens' k and v (T,Hkv,d), packed by cu_seqlens int32 (B+1,), into the pages
+    (fa_cache_append): the last positions of sequences of length seqlens (which include them).
+    Pools (num_pages,Hkv,page_size,d) bf16, or uint8 E4M3 with k_scale / v_scale fp32 (Hkv,)."""
+    dev = kpages.device
+    (pk, sk), (pv, sv), ptrs, (T, B, Hkv, num_pages, page_size, max_pages, d) = _destination(
+        k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev)
+    if T == 0:
+        return
+    _launch(load().fa_cache_append, dev, stream, pk, pv, *ptrs, T, B, Hkv, num_pages, page_size, max_pages, d, sk, sv)
+
+
+def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                inv_freq: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor, block_table: torch.Tensor,
+                cu_seqlens: torch.Tensor, seqlens: torch.Tensor, axes: Optional[torch.Tensor] = None,
+                interleaved: bool = False, k_scale: Optional[torch.Tensor] = None,
+                v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
+    """rope of q and k and cache_append of the rotated k and of v in one launch
+    (fa_rope_append).  Returns q_out (None if q is None)."""
+    dev = kpages.device
+    (pk, sk), (pv, sv), ptrs, (T, B, Hkv, num_pages, page_size, max_pages, d) = _destination(
+        k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev)
+    pq = po = None
+    sq = so = Hq = 0
+    if q is not None:
+        pq, sq = _rows(q, "q", _BF16, dev)
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q and k must have the same tokens and head dim")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        po, so = _rows(q_out, "q_out", _BF16, dev)
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out must have shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, d, dev)
+    if T == 0:
+        return q_out
+    _launch(load().fa_rope_append, dev, stream, pq, pk, pv, po, pp, pf, pa, *ptrs, T, B, Hq, Hkv, num_pages,
+            page_size, max_pages, d, F, A, sq, sk, sv, so, int(bool(interleaved)))
+    return q_out
+
+
+def _page_state(block_table, seqlens, refcount):
+    dev = block_table.device if isinstance(block_table, torch.Tensor) else None
+    ptrs = (_tensor(block_table, "block_table", torch.int32, 2), _tensor(seqlens, "seqlens", torch.int32, 1, dev),
+            _tensor(refcount, "refcount", torch.int32, 1, dev))
+    S, max_pages = block_table.shape
+    if seqlens.shape[0] != S:
+        raise ValueError("block_table and seqlens must have the same number of slots")
+    return dev, ptrs, (S, max_pages, refcount.shape[0])
+
+
+def _list(t, name, n, dev):
+    p = _tensor(t, name, torch.int32, 1, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    return p
+
+
+def _copies(copies, n, dev):
+    if copies is None:
+        copies = torch.empty((n, 2), dtype=torch.int32, device=dev)
+    p = _tensor(copies, "copies", torch.int32, 2, dev)
+    if tuple(copies.shape) != (n, 2):
+        raise ValueError(f"copies must have shape {(n, 2)}, got {tuple(copies.shape)}")
+    return p, copies
+
+
+def pages_reserve_workspace_size(S: int, num_pages: int) -> int:
+    return int(load().fa_pages_reserve_workspace_size(S, num_pages))
+
+
+def pages_compact_workspace_size(num_pages: int) -> int:
+    return int(load().fa_pages_compact_workspace_size(num_pages))
+
+
+def pages_reserve(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, add: torch.Tensor,
+                  page_size: int, copies: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Lengthen every slot s by add[s] tokens (fa_pages_reserve).  Returns copies int32 (S,2):
+    {old, new} for each shared last page that was split, else -1; pass it to pages_copy for
+    every layer's pools.  Too few free pages: nothing changes, get_error() says so."""
+    dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
+    pa = _list(add, "add", S, dev)
+    pc, copies = _copies(copies, S, dev)
+    pw, nw, workspace = _scratch(workspace, pages_reserve_workspace_size(S, num_pages), dev)
+    _launch(load().fa_pages_reserve, dev, stream, *state, pa, pc, S, max_pages, num_pages, int(page_size), pw, nw)
+    return copies
+
+
+def pages_fork(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, src: torch.Tensor,
+               dst: torch.Tensor, page_size: int, lengths: Optional[torch.Tensor] = None, stream=None):
+    """Empty slots dst become the first lengths[i] tokens (None: all) of slots src, sharing
+    their pages (fa_pages_fork)."""
+    dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
+    ps = _tensor(src, "src", torch.int32, 1, dev)
+    n = src.shape[0]
+    pd = _list(dst, "dst", n, dev)
+    pl = _list(lengths, "lengths", n, dev) if lengths is not None else None
+    if n == 0:
+        return
+    _launch(load().fa_pages_fork, dev, stream, *state, ps, pd, pl, n, S, max_pages, num_pages, int(page_size))
+
+
+def pages_free(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, slots: torch.Tensor,
+               page_size: int, keep: Optional[torch.Tensor] = None, stream=None):
+    """Cut the listed slots to their first keep[i] tokens (None: none) and give back the pages
+    behind them (fa_pages_free)."""
+    dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
+    ps = _tensor(slots, "slots", torch.int32, 1, dev)
+    n = slots.shape[0]
+    pk = _list(keep, "keep", n, dev) if keep is not None else None
+    if n == 0:
+        return
+    _launch(load().fa_pages_free, dev, stream, *state, ps, pk, n, S, max_pages, num_pages, int(page_size))
+
+
+def pages_compact(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, page_size: int,
+                  copies: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Move the live pages to the front of the pool (fa_pages_compact).  Returns copies int32
+    (num_pages // 2, 2), {from, to} and -1 behind the last move, for pages_copy."""
+    dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
+    pc, copies = _copies(copies, num_pages // 2, dev)
+    pw, nw, workspace = _scratch(workspace, pages_compact_workspace_size(num_pages), dev)
+    _launch(load().fa_pages_compact, dev, stream, *state, pc, S, max_pages, num_pages, int(page_size), pw, nw)
+    return copies
+
+
+def pages_copy(kpages: torch.Tensor, vpages: Optional[torch.Tensor], copies: torch.Tensor, stream=None):
+    """Copy page copies[i,0] to page copies[i,1] in both pools (fa_pages_copy); -1 is skipped.
+    Pools (num_pages,Hkv,page_size,d), bf16 or uint8."""
+    if not isinstance(kpages, torch.Tensor):
+        raise TypeError("kpages must be a torch.Tensor")
+    dev, dtype = kpages.device, kpages.dtype
+    if dtype not in (torch.bfloat16, torch.uint8):
+        raise ValueError(f"kpages must be bfloat16 or uint8, got {dtype}")
+    pk = _tensor(kpages, "kpages", dtype, 4)
+    pv = None
+    if vpages is not None:
+        pv = _tensor(vpages, "vpages", dtype, 4, dev)
+        if vpages.shape != kpages.shape:
+            raise ValueError("kpages and vpages must have the same shape")
+    pc = _tensor(copies, "copies", torch.int32, 2, dev)
+    if copies.shape[1] != 2:
+        raise ValueError(f"copies must have shape (n, 2), got {tuple(copies.shape)}")
+    num_pages, Hkv, page_size, d = kpages.shape
+    if copies.shape[0] == 0:
+        return
+    _launch(load().fa_pages_copy, dev, stream, pk, pv, pc, copies.shape[0], num_pages,
+            Hkv * page_size * d * kpages.element_size())
 
 
 def get_error(stream=None) -> int:

@@ -50,9 +50,12 @@ typedef enum {
     FA_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed; see fa_last_error_message */
     FA_ERR_TIMEOUT = 5,      /* a kernel pipeline wait exceeded its time limit (fa_get_error) */
     FA_ERR_DEVICE_ARG = 6,   /* the device found seqlens[b] outside [0, Nmax] and clamped it,
-                                or a block-table entry outside the page pool */
-    FA_ERR_DEBUG_CHECK = 7   /* debug builds only: a global-memory index computed by a kernel
+                                a block-table entry outside the page pool, or another value in
+                                device memory that its call refuses */
+    FA_ERR_DEBUG_CHECK = 7,  /* debug builds only: a global-memory index computed by a kernel
                                 failed its bounds check; the access was skipped */
+    FA_ERR_NO_PAGES = 8      /* fa_pages_reserve found fewer free pages than it needed and
+                                changed nothing (fa_get_error) */
 } fa_status;
 
 typedef enum { FA_BF16 = 0, FA_F32 = 1 } fa_dtype;
@@ -272,9 +275,118 @@ FA_API int fa_decode_noalloc(const void *q, const void *kcache, const void *vcac
                              int Nmax, int d, float scale, void *stream);
 
 /*
+ * Rotary positions with one or several axes.  Token t carries A positions (one axis for
+ * text; time, height and width for images and video); frequency f belongs to axis axes[f]
+ * and turns one pair (x, y) of every head's elements by a = positions[axes[f]][t] *
+ * inv_freq[f]:  x' = x cos a - y sin a,  y' = x sin a + y cos a.
+ *   q (T, Hq, d), k (T, Hkv, d): bf16 or fp32 (dtype FA_BF16, FA_F32), the heads of a token
+ *             contiguous, consecutive tokens q_stride / k_stride elements apart (slices of a
+ *             fused projection need no copy).  Hq or Hkv may be 0 (its pointers are unused).
+ *   q_out, k_out: as q and k, with strides of their own; either may be its input (in place),
+ *             any other overlap is undefined.
+ *   positions int32 (A, T), inv_freq fp32 (F), axes int32 (F) or NULL (one axis): device.  An
+ *             axis outside [0, A) is reported by fa_get_error (FA_ERR_DEVICE_ARG).
+ *   F         frequencies, 1 .. d / 2; elements from 2 F on are copied (partial rotary).
+ *   interleaved: 0 pairs elements (f, f + F), otherwise (2 f, 2 f + 1).
+ *   inverse != 0 rotates by -a: the transpose, so the gradient with respect to q and k is
+ *             fa_rope of the gradients with inverse set; it also undoes a rotation.
+ * Angles are formed and reduced in 64 bits (exact for far positions), the rotation runs in
+ * fp32 and is rounded once.  Supported: d in {64, 128}; strides multiples of 16 bytes and
+ * pointers 16-byte aligned (FA_ERR_UNSUPPORTED otherwise).
+ */
+FA_API int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *positions,
+                   const float *inv_freq, const int *axes, int T, int Hq, int Hkv, int d, int F, int A,
+                   long long q_stride, long long k_stride, long long q_out_stride, long long k_out_stride,
+                   int dtype, int interleaved, int inverse, void *stream);
+
+/*
+ * Put the keys and values of T new tokens, packed sequence after sequence, into the pages of
+ * fa_decode_paged / fa_fwd_varlen_paged: token i of sequence b (packed row cu_seqlens[b] + i)
+ * goes to position seqlens[b] - n_b + i of that sequence, n_b = cu_seqlens[b + 1] -
+ * cu_seqlens[b]; seqlens are the lengths that include the new tokens (as fa_pages_reserve
+ * leaves them).  One token per sequence (cu_seqlens = 0, 1, ..., B) is a decode step.
+ *   k, v      (T, Hkv, d) bf16, token strides k_stride / v_stride in elements
+ *   kpages, vpages (num_pages, Hkv, page_size, d) bf16; with k_scale and v_scale (fp32 Hkv,
+ *             both or neither) E4M3 bytes, byte = e4m3(value / scale[head]) rounded to nearest
+ *             even and saturated, d = 128
+ *   block_table int32 (B, max_pages), cu_seqlens int32 (B + 1) ascending from 0, seqlens
+ *             int32 (B): device.  A token whose position or page does not exist is not
+ *             written and reported by fa_get_error (FA_ERR_DEVICE_ARG); rows from
+ *             cu_seqlens[B] on (padding) are skipped.
+ *   page_size a multiple of 16 (FA_ERR_UNSUPPORTED otherwise).
+ * Two tokens must not go to the same row of the same page (pages shared by several sequences
+ * hold only finished positions; fa_pages_reserve sees to that).
+ */
+FA_API int fa_cache_append(const void *k, const void *v, void *kpages, void *vpages, const float *k_scale,
+                           const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens,
+                           int T, int B, int Hkv, int num_pages, int page_size, int max_pages, int d,
+                           long long k_stride, long long v_stride, void *stream);
+
+/*
+ * fa_rope of q and k and fa_cache_append of the rotated k and of v in one launch: q_out gets
+ * the rotated q (rows from cu_seqlens[B] on are left as they were), the pages get the rotated
+ * keys (rounded once, to the cache's type) and the values.  Hq may be 0.  Arguments as in
+ * those calls (bf16 q, k, v).
+ */
+FA_API int fa_rope_append(const void *q, const void *k, const void *v, void *q_out, const int *positions,
+                          const float *inv_freq, const int *axes, void *kpages, void *vpages, const float *k_scale,
+                          const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens,
+                          int T, int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages, int d, int F,
+                          int A, long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
+                          int interleaved, void *stream);
+
+/*
+ * Page management.  The state is the caller's, in device memory:
+ *   block_table int32 (S, max_pages) and seqlens int32 (S), as the paged attention reads
+ *   them: a slot of length L holds ceil(L / page_size) pages;
+ *   refcount int32 (num_pages): the number of table entries that name a page, plus any holds
+ *   of the caller's own; 0 is free.
+ * All start as zeros.  Every call enqueues on `stream`, reads its lists from device memory and
+ * changes the state in place; calls on one state must be ordered.  What a call refuses (a slot
+ * out of range, a destination that is not empty, a length that a slot does not have, a slot
+ * listed twice) is left out and reported by fa_get_error as FA_ERR_DEVICE_ARG.  The result
+ * depends on state and arguments alone: free pages are handed out lowest first, slot by slot.
+ * page_size is a multiple of 16, num_pages < 2^21 - 1, S <= 2^20.
+ *
+ * fa_pages_reserve: lengthens slot s by add[s] >= 0 tokens (int32 S): seqlens grows, new pages
+ *   go to the end of the row, and a last page that is partly filled and shared (refcount > 1
+ *   at the start of the call) is replaced by a page of the slot's own: copies[s] (int32 (S, 2))
+ *   is then {old page, new page} for fa_pages_copy, otherwise {-1, -1}.  All or nothing: with
+ *   too few free pages (FA_ERR_NO_PAGES) or a slot that cannot grow so (FA_ERR_DEVICE_ARG)
+ *   nothing changes and copies is all -1.  workspace: 16-byte aligned device scratch of
+ *   fa_pages_reserve_workspace_size(S, num_pages) bytes; calls that share it must be ordered.
+ * fa_pages_fork: for each of n pairs, the empty slot dst[i] becomes the first lengths[i]
+ *   tokens of src[i] (lengths NULL: all); its pages are shared, no data moves.  A slot listed
+ *   as a destination may not also be a source.  n <= 65535.
+ * fa_pages_free: cuts each of n listed slots to its first keep[i] tokens (keep NULL: none) and
+ *   gives back the pages behind them; their table entries become -1.  n <= 65535.
+ * fa_pages_compact: moves the live pages to the front of the pool: with m live pages, the k-th
+ *   live page at or behind m goes to the k-th free page before m.  Tables and refcounts follow;
+ *   copies (int32 (num_pages / 2, 2)) lists the moves, {-1, -1} behind the last.  Workspace as
+ *   above, fa_pages_compact_workspace_size(num_pages) bytes.
+ * fa_pages_copy: copies page copies[i][0] to page copies[i][1] (n entries, device memory) in
+ *   kpages and, when not NULL, vpages; {-1, -1} is skipped.  page_bytes = Hkv * page_size * d *
+ *   element size, a multiple of 16.  No destination may be listed twice or be a source (the
+ *   lists above never do so).  Call it once per layer's pools after reserve or compact.
+ */
+FA_API size_t fa_pages_reserve_workspace_size(int S, int num_pages);
+FA_API int fa_pages_reserve(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int S,
+                            int max_pages, int num_pages, int page_size, void *workspace, size_t workspace_bytes,
+                            void *stream);
+FA_API int fa_pages_fork(int *block_table, int *seqlens, int *refcount, const int *src, const int *dst,
+                         const int *lengths, int n, int S, int max_pages, int num_pages, int page_size, void *stream);
+FA_API int fa_pages_free(int *block_table, int *seqlens, int *refcount, const int *slots, const int *keep, int n,
+                         int S, int max_pages, int num_pages, int page_size, void *stream);
+FA_API size_t fa_pages_compact_workspace_size(int num_pages);
+FA_API int fa_pages_compact(int *block_table, int *seqlens, int *refcount, int *copies, int S, int max_pages,
+                            int num_pages, int page_size, void *workspace, size_t workspace_bytes, void *stream);
+FA_API int fa_pages_copy(void *kpages, void *vpages, const int *copies, int n, int num_pages, long long page_bytes,
+                         void *stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word.  Returns FA_OK,
- * FA_ERR_TIMEOUT, FA_ERR_DEVICE_ARG, FA_ERR_DEBUG_CHECK (debug builds), or FA_ERR_CUDA if
- * the synchronisation itself failed.
+ * FA_ERR_TIMEOUT, FA_ERR_DEVICE_ARG, FA_ERR_NO_PAGES, FA_ERR_DEBUG_CHECK (debug builds), or
+ * FA_ERR_CUDA if the synchronisation itself failed.
  */
 FA_API int fa_get_error(void *stream);
 
