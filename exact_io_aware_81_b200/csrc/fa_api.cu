@@ -18,6 +18,7 @@
 #include "fa_pages_sm100.cuh"
 #include "fa_prefill_sm100.cuh"
 #include "fa_rope_sm100.cuh"
+#include "fa_varlen_sm100.cuh"
 
 namespace {
 
@@ -52,6 +53,7 @@ struct DeviceInfo {
     int num_sms = 0;
     bool prefill_attr_set[2][2][2][2][2] = {};
     bool decode_attr_set[2][4][2][2] = {};
+    bool varlen_attr_set[2][2][2][2] = {};
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -511,6 +513,214 @@ int decode_general(const void *q, const CacheDesc &c, const int *seqlens, void *
 
 }  // namespace
 
+// ------------------------------------------------- attention over packed sequences
+
+namespace {
+
+constexpr int kVarlenHeadBytes = 256;
+// K and V bytes that the units running at one time share through L2 (126 MB, of which Q, O
+// and the other die's copies take their part)
+constexpr long long kSectionBytes = 40LL << 20;
+
+int check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (!ws || have < need) return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, have);
+    if (!aligned16(ws)) return fail(FA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    return FA_OK;
+}
+
+size_t varlen_ws_bytes(int B, int Tq)
+{
+    if (B <= 0 || Tq <= 0) return 0;
+    return kVarlenHeadBytes + ((size_t)Tq / 128 + B) * 32;
+}
+
+// The attention kernel is a programmatic dependent of the plan kernel: its set-up runs while
+// the plan is made.
+template <int D, bool F32, bool SPLIT, int LAYOUT>
+int launch_varlen(const fa::PrefillParams &p, int grid, DeviceInfo *info, cudaStream_t st)
+{
+    using C = fa::prefill::Cfg<D, false>;
+    static_assert(C::kSmemBytes <= 227 * 1024, "prefill shared memory");
+    auto kern = fa::fa_prefill_kernel<D, F32, SPLIT, true, false, LAYOUT>;
+    {
+        std::lock_guard<std::mutex> lk(g_dev_mu);
+        bool &set = info->varlen_attr_set[D == 128][F32][SPLIT][LAYOUT == fa::kPaged];
+        if (!set) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+            if (e != cudaSuccess) return fail(FA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            set = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(fa::prefill::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return fail(FA_ERR_CUDA, "packed attention launch: %s", cudaGetErrorString(e));
+    return FA_OK;
+}
+
+template <int LAYOUT>
+int launch_varlen_variant(const fa::PrefillParams &p, int d, bool f32, int grid, DeviceInfo *info, cudaStream_t st)
+{
+    if (d == 128) {
+        if (f32) return p.head_pair ? launch_varlen<128, true, true, LAYOUT>(p, grid, info, st)
+                                    : launch_varlen<128, true, false, LAYOUT>(p, grid, info, st);
+        return p.head_pair ? launch_varlen<128, false, true, LAYOUT>(p, grid, info, st)
+                           : launch_varlen<128, false, false, LAYOUT>(p, grid, info, st);
+    }
+    if (f32) return p.head_pair ? launch_varlen<64, true, true, LAYOUT>(p, grid, info, st)
+                                : launch_varlen<64, true, false, LAYOUT>(p, grid, info, st);
+    return p.head_pair ? launch_varlen<64, false, true, LAYOUT>(p, grid, info, st)
+                       : launch_varlen<64, false, false, LAYOUT>(p, grid, info, st);
+}
+
+// Packed rows (T, heads, d), tokens `stride` elements apart, as the 4-D (d, rows, heads, 1)
+// map of the prefill kernel.
+int encode_packed_map(CUtensorMap *m, const void *base, int D, long long rows, int heads, long long stride,
+                      unsigned box_rows = 128)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads, 1};
+    const cuuint64_t strides[3] = {(cuuint64_t)stride * 2, (cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[4] = {64, box_rows, 1, 1};
+    return encode_map_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box);
+}
+
+// The keys of a packed call: packed tensors, or pages.
+struct VarlenKeys {
+    const void *k, *v;
+    const int *cu_k;
+    int Tk;
+    long long k_stride, v_stride;
+    bool paged;
+    const int *block_table, *seqlens;
+    int num_pages, page_size, max_pages;
+};
+
+bool token_stride_ok(long long stride, int heads, int d) { return stride >= (long long)heads * d && stride % 8 == 0; }
+
+int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o, float *lse, int B, int Tq, int Hq,
+                   int Hkv, int d, long long q_stride, float scale, int causal, int window, int o_dtype,
+                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!q || !o || !lse || !cu_q) return fail(FA_ERR_INVALID, "null pointer argument");
+    if (c.paged ? (!c.k || !c.v || !c.block_table || !c.seqlens) : (!c.cu_k || (c.Tk > 0 && (!c.k || !c.v))))
+        return fail(FA_ERR_INVALID, "null pointer argument");
+    if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || c.Tk < 0)
+        return fail(FA_ERR_INVALID, "sizes must be positive (B=%d Tq=%d Tk=%d Hq=%d Hkv=%d d=%d)", B, Tq, c.Tk, Hq, Hkv, d);
+    if (c.paged && (c.num_pages <= 0 || c.page_size <= 0 || c.max_pages <= 0))
+        return fail(FA_ERR_INVALID, "page sizes must be positive (num_pages=%d page_size=%d max_pages=%d)", c.num_pages,
+                    c.page_size, c.max_pages);
+    if (Hq % Hkv != 0) return fail(FA_ERR_INVALID, "Hq (%d) must be a multiple of Hkv (%d)", Hq, Hkv);
+    if (!(scale > 0.f) || !std::isfinite(scale)) return fail(FA_ERR_INVALID, "scale must be finite and > 0");
+    if (o_dtype != FA_BF16 && o_dtype != FA_F32) return fail(FA_ERR_INVALID, "unknown output dtype %d", o_dtype);
+    if (window < 0) return fail(FA_ERR_INVALID, "window must be >= 0 (got %d)", window);
+    if (window > 0 && !causal) return fail(FA_ERR_INVALID, "a sliding window needs causal attention");
+    if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", d);
+    if (!token_stride_ok(q_stride, Hq, d) ||
+        (!c.paged && c.Tk > 0 && (!token_stride_ok(c.k_stride, Hkv, d) || !token_stride_ok(c.v_stride, Hkv, d))))
+        return fail(FA_ERR_UNSUPPORTED, "a token stride must hold the heads and be a multiple of 16 bytes");
+    if (c.paged && c.page_size % 16 != 0)
+        return fail(FA_ERR_UNSUPPORTED, "page_size %d is not a multiple of 16", c.page_size);
+    if (!aligned16(q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(o))
+        return fail(FA_ERR_UNSUPPORTED, "q, k, v and o must be 16-byte aligned");
+    if (B > fa::varlen::kMaxSeqs) return fail(FA_ERR_UNSUPPORTED, "at most %d sequences in one call (%d)", fa::varlen::kMaxSeqs, B);
+    const long long keys = c.paged ? (long long)c.page_size * c.max_pages : c.Tk;
+    const int R = Hq / Hkv;
+    const bool pair = R % 2 == 0;
+    const int slots = pair ? Hq / 2 : Hq;
+    const long long units = ((long long)Tq / 128 + B) * slots;
+    if (Tq >= (1 << 26) || keys >= (1 << 30) || units > 0x3fffffffLL ||
+        (c.paged && (long long)c.num_pages * Hkv > 0x3fffffffLL))
+        return fail(FA_ERR_UNSUPPORTED, "problem too large");
+    int rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, varlen_ws_bytes(B, Tq))) != FA_OK) return rc;
+    int dev;
+    DeviceInfo *info;
+    if ((rc = current_device(&dev, &info)) != FA_OK) return rc;
+
+    fa::PrefillParams p;
+    memset(&p, 0, sizeof p);
+    if ((rc = encode_packed_map(&p.tm_q, q, d, Tq, Hq, q_stride)) != FA_OK) return rc;
+    if (c.paged) {
+        p.box_rows = c.page_size & -c.page_size;
+        if (p.box_rows > 128) p.box_rows = 128;
+        const long long planes = (long long)c.num_pages * Hkv;
+        if ((rc = encode_rows_map(&p.tm_k, c.k, d, c.page_size, planes, p.box_rows)) != FA_OK) return rc;
+        if ((rc = encode_rows_map(&p.tm_v, c.v, d, c.page_size, planes, p.box_rows)) != FA_OK) return rc;
+        p.block_table = c.block_table;
+        p.page_size = c.page_size;
+        p.max_pages = c.max_pages;
+        p.num_pages = c.num_pages;
+    } else {
+        // without a single key every tile is masked and its values cleared: any memory does
+        const bool none = c.Tk == 0;
+        if ((rc = encode_packed_map(&p.tm_k, none ? q : c.k, d, none ? Tq : c.Tk, Hkv, none ? q_stride : c.k_stride)) != FA_OK ||
+            (rc = encode_packed_map(&p.tm_v, none ? q : c.v, d, none ? Tq : c.Tk, Hkv, none ? q_stride : c.v_stride)) != FA_OK)
+            return rc;
+    }
+    if (o_dtype == FA_BF16 && (rc = encode_packed_map(&p.tm_o, o, d, Tq, Hq, (long long)Hq * d, 32)) != FA_OK) return rc;
+    p.o = o;
+    p.o_sh = d;
+    p.o_sn = (long long)Hq * d;
+    p.lse = lse;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.Nq = Tq;
+    p.Nk = (int)keys;
+    p.R = R;
+    p.causal = causal ? 1 : 0;
+    p.window = window;
+    p.head_pair = pair ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.wait_limit_ns = g_wait_limit_ns;
+    p.slots = slots;
+    p.slots_per_group = pair ? R / 2 : R;
+    long long pool_keys = c.paged ? (long long)c.page_size * c.num_pages : keys;
+    if (c.paged && pool_keys > keys * B) pool_keys = keys * B;
+    long long groups = pool_keys > 0 ? kSectionBytes / (pool_keys * d * 4) : Hkv;
+    groups = groups < 1 ? 1 : groups > Hkv ? Hkv : groups;
+    p.section_slots = (int)groups * p.slots_per_group;
+    p.plan_head = static_cast<int *>(workspace);
+    int4 *plan = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + kVarlenHeadBytes);
+    p.plan = plan;
+
+    fa::VarlenPlanParams m;
+    m.cu_q = cu_q;
+    m.cu_k = c.cu_k;
+    m.seqlens = c.paged ? c.seqlens : nullptr;
+    m.plan = plan;
+    m.head = p.plan_head;
+    m.B = B;
+    m.Tq = Tq;
+    m.Tk = (int)keys;
+    m.rows = pair ? 128 : 256;
+    m.causal = p.causal;
+    m.window = window;
+    m.max_jobs = Tq / m.rows + B;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    fa::fa_varlen_plan_kernel<<<1, fa::varlen::kThreads, 0, st>>>(m);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(FA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));
+    const long long bound = (long long)m.max_jobs * slots;
+    const int grid = bound < info->num_sms ? (int)bound : info->num_sms;
+    const bool f32 = o_dtype == FA_F32;
+    rc = c.paged ? launch_varlen_variant<fa::kPaged>(p, d, f32, grid, info, st)
+                 : launch_varlen_variant<fa::kPacked>(p, d, f32, grid, info, st);
+    if (rc != FA_OK) return rc;
+    return ok();
+}
+
+}  // namespace
+
 // ---------------------------------------------- rotary positions and cache filling
 
 namespace {
@@ -656,13 +866,6 @@ size_t compact_ws_bytes(int num_pages)
 {
     if (num_pages <= 0) return 0;
     return 256 + 2 * align256((size_t)num_pages * 4);
-}
-
-int check_workspace(const void *ws, size_t have, size_t need)
-{
-    if (!ws || have < need) return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, have);
-    if (!aligned16(ws)) return fail(FA_ERR_WORKSPACE, "workspace must be 16-byte aligned");
-    return FA_OK;
 }
 
 int launched(const char *what)
@@ -899,6 +1102,28 @@ int fa_decode_noalloc(const void *q, const void *kcache, const void *vcache, con
 }
 
 // ---------------------------------------------- rotary positions and cache filling
+
+size_t fa_fwd_varlen_workspace_size(int B, int Tq) { return varlen_ws_bytes(B, Tq); }
+
+int fa_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q, const int *cu_k,
+                  int B, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride, long long k_stride,
+                  long long v_stride, float scale, int causal, int window, int o_dtype, void *workspace,
+                  size_t workspace_bytes, void *stream)
+{
+    const VarlenKeys c{k, v, cu_k, Tk, k_stride, v_stride, false, nullptr, nullptr, 0, 0, 0};
+    return varlen_general(q, c, cu_q, o, lse, B, Tq, Hq, Hkv, d, q_stride, scale, causal, window, o_dtype, workspace,
+                          workspace_bytes, stream);
+}
+
+int fa_fwd_varlen_paged(const void *q, const void *kpages, const void *vpages, const int *block_table,
+                        const int *cu_q, const int *seqlens, void *o, float *lse, int B, int Tq, int Hq, int Hkv,
+                        int num_pages, int page_size, int max_pages, int d, long long q_stride, float scale,
+                        int causal, int window, int o_dtype, void *workspace, size_t workspace_bytes, void *stream)
+{
+    const VarlenKeys c{kpages, vpages, nullptr, 0, 0, 0, true, block_table, seqlens, num_pages, page_size, max_pages};
+    return varlen_general(q, c, cu_q, o, lse, B, Tq, Hq, Hkv, d, q_stride, scale, causal, window, o_dtype, workspace,
+                          workspace_bytes, stream);
+}
 
 int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *positions, const float *inv_freq,
             const int *axes, int T, int Hq, int Hkv, int d, int F, int A, long long q_stride, long long k_stride,

@@ -49,6 +49,9 @@ SIGNATURES = {
     "fa_decode_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _Z, _P]),
     "fa_decode_paged_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                  _P, _Z, _P]),
+    "fa_fwd_varlen_workspace_size": (_Z, [_I, _I]),
+    "fa_fwd_varlen": (_I, [_P] * 7 + [_I] * 6 + [_L] * 3 + [_F, _I, _I, _I, _P, _Z, _P]),
+    "fa_fwd_varlen_paged": (_I, [_P] * 8 + [_I] * 8 + [_L, _F, _I, _I, _I, _P, _Z, _P]),
     "fa_rope": (_I, [_P] * 7 + [_I] * 6 + [_L] * 4 + [_I] * 3 + [_P]),
     "fa_cache_append": (_I, [_P] * 9 + [_I] * 7 + [_L] * 2 + [_P]),
     "fa_rope_append": (_I, [_P] * 14 + [_I] * 10 + [_L] * 4 + [_I, _P]),
@@ -485,7 +488,7 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
     return out, lse
 
 
-# ------------------------------------------- rotary positions, cache filling, pages
+# --------------- packed sequences, rotary positions, cache filling, page management
 #
 # These calls are short (a few microseconds on the device), so their checks are the plain
 # ones below: one pass over each tensor's attributes, and the device is switched only when
@@ -566,6 +569,88 @@ def _rotation(positions, inv_freq, axes, T, d, dev):
 
 _ROPE_TYPES = (torch.bfloat16, torch.float32)
 _BF16 = (torch.bfloat16,)
+
+
+def varlen_workspace_size(B: int, Tq: int) -> int:
+    return int(load().fa_fwd_varlen_workspace_size(B, Tq))
+
+
+def _varlen_outputs(q, dev, out_dtype, out, lse):
+    """Pointers of o (Tq,Hq,d) and lse (Hq,Tq), new ones unless given, and the output's code."""
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    Tq, Hq, d = q.shape
+    if out is None:
+        out = torch.empty((Tq, Hq, d), dtype=out_dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
+    po, pl = _tensor(out, "out", out_dtype, 3, dev), _tensor(lse, "lse", torch.float32, 2, dev)
+    if out.shape != q.shape or tuple(lse.shape) != (Hq, Tq):
+        raise ValueError(f"out must have shape {tuple(q.shape)} and lse {(Hq, Tq)}, "
+                         f"got {tuple(out.shape)} and {tuple(lse.shape)}")
+    return po, pl, out, lse, FA_F32 if out_dtype == torch.float32 else FA_BF16
+
+
+def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+               cu_seqlens_k: Optional[torch.Tensor] = None, causal: bool = False, scale: Optional[float] = None,
+               window: int = 0, out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention over packed sequences (fa_fwd_varlen): q (Tq,Hq,d), k/v (Tk,Hkv,d) bf16, tokens
+    strided or not; cu_seqlens_q / cu_seqlens_k int32 (B+1,) on the device (the latter defaults to
+    the former).  Returns (o (Tq,Hq,d), lse fp32 (Hq,Tq)); causal is bottom-right aligned in each
+    sequence, a row that sees no key gives o = 0 and lse = -inf.  ``workspace`` is a uint8 CUDA
+    tensor of varlen_workspace_size(B, Tq) bytes; one is allocated if omitted."""
+    dev = q.device
+    pq, sq = _rows(q, "q", _BF16, dev)
+    pk, sk = _rows(k, "k", _BF16, dev)
+    pv, sv = _rows(v, "v", _BF16, dev)
+    pcq = _tensor(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+    pck = pcq if cu_seqlens_k is None else _tensor(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1, dev)
+    Tq, Hq, d = q.shape
+    Tk, Hkv, dk = k.shape
+    B = cu_seqlens_q.shape[0] - 1
+    if dk != d or v.shape != k.shape or B < 1 or (cu_seqlens_k is not None and cu_seqlens_k.shape[0] != B + 1):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)} and the cu_seqlens")
+    po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if Tq == 0:
+        return out, lse
+    pw, nw, workspace = _scratch(workspace, varlen_workspace_size(B, Tq), dev)
+    _launch(load().fa_fwd_varlen, dev, stream, pq, pk, pv, po, pl, pcq, pck, B, Tq, Tk, Hq, Hkv, d, sq, sk, sv,
+            float(scale), int(bool(causal)), int(window), odt, pw, nw)
+    return out, lse
+
+
+def fwd_varlen_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor, block_table: torch.Tensor,
+                     cu_seqlens_q: torch.Tensor, seqlens: torch.Tensor, causal: bool = True,
+                     scale: Optional[float] = None, window: int = 0, out_dtype: torch.dtype = torch.bfloat16,
+                     workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, stream=None):
+    """fwd_varlen with the keys in a paged cache (fa_fwd_varlen_paged): q (Tq,Hq,d) bf16 packed by
+    cu_seqlens_q int32 (B+1,); sequence b attends the first seqlens[b] tokens of its pages (pools
+    (num_pages,Hkv,page_size,d) bf16, block_table int32 (B,max_pages)), of which its rows are the
+    last: chunked prefill, or a prompt that continues a shared prefix."""
+    dev = q.device
+    pq, sq = _rows(q, "q", _BF16, dev)
+    pkp, pvp = _tensor(kpages, "kpages", torch.bfloat16, 4, dev), _tensor(vpages, "vpages", torch.bfloat16, 4, dev)
+    pbt = _tensor(block_table, "block_table", torch.int32, 2, dev)
+    pcq = _tensor(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
+    psl = _tensor(seqlens, "seqlens", torch.int32, 1, dev)
+    Tq, Hq, d = q.shape
+    num_pages, Hkv, page_size, dk = kpages.shape
+    B, max_pages = block_table.shape
+    if dk != d or vpages.shape != kpages.shape or seqlens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
+        raise ValueError("shape mismatch between q, kpages, vpages, block_table, cu_seqlens_q and seqlens")
+    po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if Tq == 0:
+        return out, lse
+    pw, nw, workspace = _scratch(workspace, varlen_workspace_size(B, Tq), dev)
+    _launch(load().fa_fwd_varlen_paged, dev, stream, pq, pkp, pvp, pbt, pcq, psl, po, pl, B, Tq, Hq, Hkv, num_pages,
+            page_size, max_pages, d, sq, float(scale), int(bool(causal)), int(window), odt, pw, nw)
+    return out, lse
 
 
 def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, inv_freq: torch.Tensor,

@@ -275,6 +275,48 @@ FA_API int fa_decode_noalloc(const void *q, const void *kcache, const void *vcac
                              int Nmax, int d, float scale, void *stream);
 
 /*
+ * Forward attention over packed sequences of different lengths (youngju.dev "attention
+ * variants", section 5: continuous batching puts prompts of any length into one batch), with
+ * no padding: the rows of sequence b are cu_q[b] .. cu_q[b + 1] - 1 of q, o and the LSE, its
+ * keys cu_k[b] .. cu_k[b + 1] - 1 of k and v.
+ *   q   (Tq, Hq,  d) bf16             k, v (Tk, Hkv, d) bf16
+ *   o   (Tq, Hq,  d) written, bf16 or fp32 (o_dtype);  lse (Hq, Tq) fp32 written
+ *   cu_q, cu_k int32 (B + 1), device: ascending from >= 0 to at most Tq / Tk; pass the same
+ *             pointer when queries and keys are the same tokens.  Others are forced into the
+ *             tensors and reported by fa_get_error (FA_ERR_DEVICE_ARG).
+ *   q_stride, k_stride, v_stride: elements between consecutive tokens (the heads of one token
+ *             are contiguous), at least heads * d and a multiple of 8: slices of a fused
+ *             projection need no copy.
+ *   causal, window, scale: as fa_fwd_window, per sequence, with bottom-right alignment: row i
+ *             of n sees keys j <= i + (m - n) of m.  n > m is allowed here: a row that sees no
+ *             key (also m = 0) gets o = 0, lse = -inf.  Sequences without rows are skipped.
+ * Rows of o and lse that belong to no sequence are left as they were.  Nothing of one sequence
+ * (NaN and infinities included) reaches another.
+ *   workspace: device scratch of fa_fwd_varlen_workspace_size(B, Tq) bytes, 16-byte aligned,
+ *             contents ignored and overwritten; calls that share it must be ordered.
+ * Supported: d in {64, 128}, B <= 4096, Tq < 2^26, Tk < 2^30 (FA_ERR_UNSUPPORTED otherwise).
+ */
+FA_API size_t fa_fwd_varlen_workspace_size(int B, int Tq);
+FA_API int fa_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q,
+                         const int *cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride,
+                         long long k_stride, long long v_stride, float scale, int causal, int window, int o_dtype,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * fa_fwd_varlen over a paged cache (chunked prefill, and prompts that continue a shared
+ * prefix; youngju.dev section 5): the keys of sequence b are the first seqlens[b] tokens of its
+ * pages (kpages, vpages, block_table, page_size as fa_decode_paged; seqlens include the new
+ * rows, as fa_cache_append leaves them).  What a page holds behind the last key is not used.
+ * Pages outside the pool read as zeros and are reported, as are lengths outside
+ * [0, page_size * max_pages] (FA_ERR_DEVICE_ARG).  Other arguments as fa_fwd_varlen.
+ */
+FA_API int fa_fwd_varlen_paged(const void *q, const void *kpages, const void *vpages, const int *block_table,
+                               const int *cu_q, const int *seqlens, void *o, float *lse, int B, int Tq, int Hq,
+                               int Hkv, int num_pages, int page_size, int max_pages, int d, long long q_stride,
+                               float scale, int causal, int window, int o_dtype, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
  * Rotary positions with one or several axes.  Token t carries A positions (one axis for
  * text; time, height and width for images and video); frequency f belongs to axis axes[f]
  * and turns one pair (x, y) of every head's elements by a = positions[axes[f]][t] *
