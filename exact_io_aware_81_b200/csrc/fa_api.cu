@@ -53,7 +53,7 @@ struct DeviceInfo {
     int num_sms = 0;
     bool prefill_attr_set[2][2][2][2][2] = {};
     bool decode_attr_set[2][4][2][2] = {};
-    bool varlen_attr_set[2][2][2][2] = {};
+    bool varlen_attr_set[2][2][2][2][2] = {};
 };
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
@@ -518,10 +518,6 @@ int decode_general(const void *q, const CacheDesc &c, const int *seqlens, void *
 namespace {
 
 constexpr int kVarlenHeadBytes = 256;
-// K and V bytes that the units running at one time share through L2 (126 MB, of which Q, O
-// and the other die's copies take their part)
-constexpr long long kSectionBytes = 40LL << 20;
-
 int check_workspace(const void *ws, size_t have, size_t need)
 {
     if (!ws || have < need) return fail(FA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, have);
@@ -529,23 +525,34 @@ int check_workspace(const void *ws, size_t have, size_t need)
     return FA_OK;
 }
 
-size_t varlen_ws_bytes(int B, int Tq)
+// Query heads of one K/V head that share a tile: the largest divisor of R up to 32 (so that a
+// job holds at least 8 tokens).
+int varlen_pack(int R)
 {
-    if (B <= 0 || Tq <= 0) return 0;
-    return kVarlenHeadBytes + ((size_t)Tq / 128 + B) * 32;
+    for (int p = R < 32 ? R : 32; p > 1; --p)
+        if (R % p == 0) return p;
+    return 1;
+}
+
+int varlen_max_jobs(int B, int Tq, int pack) { return Tq / (2 * (128 / pack)) + B; }
+
+size_t varlen_ws_bytes(int B, int Tq, int Hq, int Hkv)
+{
+    if (B <= 0 || Tq <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    return kVarlenHeadBytes + (size_t)varlen_max_jobs(B, Tq, varlen_pack(Hq / Hkv)) * 32;
 }
 
 // The attention kernel is a programmatic dependent of the plan kernel: its set-up runs while
 // the plan is made.
-template <int D, bool F32, bool SPLIT, int LAYOUT>
-int launch_varlen(const fa::PrefillParams &p, int grid, DeviceInfo *info, cudaStream_t st)
+template <int D, bool F32, bool WINDOW, bool PAGED, bool SHORT>
+int launch_varlen(const fa::VarlenParams &p, int grid, DeviceInfo *info, cudaStream_t st)
 {
-    using C = fa::prefill::Cfg<D, false>;
-    static_assert(C::kSmemBytes <= 227 * 1024, "prefill shared memory");
-    auto kern = fa::fa_prefill_kernel<D, F32, SPLIT, true, false, LAYOUT>;
+    using C = fa::varlen::Cfg<D, SHORT>;
+    static_assert(C::kSmemBytes <= 227 * 1024, "packed attention shared memory");
+    auto kern = fa::fa_varlen_kernel<D, F32, WINDOW, PAGED, SHORT>;
     {
         std::lock_guard<std::mutex> lk(g_dev_mu);
-        bool &set = info->varlen_attr_set[D == 128][F32][SPLIT][LAYOUT == fa::kPaged];
+        bool &set = info->varlen_attr_set[D == 128][F32][WINDOW][PAGED][SHORT];
         if (!set) {
             cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
             if (e != cudaSuccess) return fail(FA_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
@@ -554,7 +561,7 @@ int launch_varlen(const fa::PrefillParams &p, int grid, DeviceInfo *info, cudaSt
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(fa::prefill::kThreads);
+    cfg.blockDim = dim3(fa::varlen::kAttnThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -567,29 +574,45 @@ int launch_varlen(const fa::PrefillParams &p, int grid, DeviceInfo *info, cudaSt
     return FA_OK;
 }
 
-template <int LAYOUT>
-int launch_varlen_variant(const fa::PrefillParams &p, int d, bool f32, int grid, DeviceInfo *info, cudaStream_t st)
+template <int D, bool F32, bool PAGED>
+int launch_varlen_sized(const fa::VarlenParams &p, bool few, int grid, DeviceInfo *info, cudaStream_t st)
 {
-    if (d == 128) {
-        if (f32) return p.head_pair ? launch_varlen<128, true, true, LAYOUT>(p, grid, info, st)
-                                    : launch_varlen<128, true, false, LAYOUT>(p, grid, info, st);
-        return p.head_pair ? launch_varlen<128, false, true, LAYOUT>(p, grid, info, st)
-                           : launch_varlen<128, false, false, LAYOUT>(p, grid, info, st);
-    }
-    if (f32) return p.head_pair ? launch_varlen<64, true, true, LAYOUT>(p, grid, info, st)
-                                : launch_varlen<64, true, false, LAYOUT>(p, grid, info, st);
-    return p.head_pair ? launch_varlen<64, false, true, LAYOUT>(p, grid, info, st)
-                       : launch_varlen<64, false, false, LAYOUT>(p, grid, info, st);
+    if (few)
+        return p.window > 0 ? launch_varlen<D, F32, true, PAGED, true>(p, grid, info, st)
+                            : launch_varlen<D, F32, false, PAGED, true>(p, grid, info, st);
+    return p.window > 0 ? launch_varlen<D, F32, true, PAGED, false>(p, grid, info, st)
+                        : launch_varlen<D, F32, false, PAGED, false>(p, grid, info, st);
+}
+
+template <bool PAGED>
+int launch_varlen_variant(const fa::VarlenParams &p, int d, bool f32, bool few, int grid, DeviceInfo *info,
+                          cudaStream_t st)
+{
+    if (d == 128)
+        return f32 ? launch_varlen_sized<128, true, PAGED>(p, few, grid, info, st)
+                   : launch_varlen_sized<128, false, PAGED>(p, few, grid, info, st);
+    return f32 ? launch_varlen_sized<64, true, PAGED>(p, few, grid, info, st)
+               : launch_varlen_sized<64, false, PAGED>(p, few, grid, info, st);
+}
+
+// The same rows as a (d, heads, tokens, 1) map with boxes of `pack` heads of `tokens` tokens:
+// the tile's rows are then token by token, head by head.
+int encode_token_map(CUtensorMap *m, const void *base, int D, long long rows, int heads, long long stride, int pack,
+                     int tokens)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows, 1};
+    const cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)pack, (cuuint32_t)tokens, 1};
+    return encode_map_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box);
 }
 
 // Packed rows (T, heads, d), tokens `stride` elements apart, as the 4-D (d, rows, heads, 1)
 // map of the prefill kernel.
-int encode_packed_map(CUtensorMap *m, const void *base, int D, long long rows, int heads, long long stride,
-                      unsigned box_rows = 128)
+int encode_packed_map(CUtensorMap *m, const void *base, int D, long long rows, int heads, long long stride)
 {
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)rows, (cuuint64_t)heads, 1};
     const cuuint64_t strides[3] = {(cuuint64_t)stride * 2, (cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-    const cuuint32_t box[4] = {64, box_rows, 1, 1};
+    const cuuint32_t box[4] = {64, 128, 1, 1};
     return encode_map_cached(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box);
 }
 
@@ -634,21 +657,20 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     if (B > fa::varlen::kMaxSeqs) return fail(FA_ERR_UNSUPPORTED, "at most %d sequences in one call (%d)", fa::varlen::kMaxSeqs, B);
     const long long keys = c.paged ? (long long)c.page_size * c.max_pages : c.Tk;
     const int R = Hq / Hkv;
-    const bool pair = R % 2 == 0;
-    const int slots = pair ? Hq / 2 : Hq;
-    const long long units = ((long long)Tq / 128 + B) * slots;
+    const int pack = varlen_pack(R), slots = Hq / pack;
+    const long long units = ((long long)Tq / (2 * (128 / pack)) + B) * slots;
     if (Tq >= (1 << 26) || keys >= (1 << 30) || units > 0x3fffffffLL ||
         (c.paged && (long long)c.num_pages * Hkv > 0x3fffffffLL))
         return fail(FA_ERR_UNSUPPORTED, "problem too large");
     int rc;
-    if ((rc = check_workspace(workspace, workspace_bytes, varlen_ws_bytes(B, Tq))) != FA_OK) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, varlen_ws_bytes(B, Tq, Hq, Hkv))) != FA_OK) return rc;
     int dev;
     DeviceInfo *info;
     if ((rc = current_device(&dev, &info)) != FA_OK) return rc;
 
-    fa::PrefillParams p;
+    fa::VarlenParams p;
     memset(&p, 0, sizeof p);
-    if ((rc = encode_packed_map(&p.tm_q, q, d, Tq, Hq, q_stride)) != FA_OK) return rc;
+    if ((rc = encode_token_map(&p.tm_q, q, d, Tq, Hq, q_stride, pack, 128 / pack)) != FA_OK) return rc;
     if (c.paged) {
         p.box_rows = c.page_size & -c.page_size;
         if (p.box_rows > 128) p.box_rows = 128;
@@ -666,29 +688,23 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
             (rc = encode_packed_map(&p.tm_v, none ? q : c.v, d, none ? Tq : c.Tk, Hkv, none ? q_stride : c.v_stride)) != FA_OK)
             return rc;
     }
-    if (o_dtype == FA_BF16 && (rc = encode_packed_map(&p.tm_o, o, d, Tq, Hq, (long long)Hq * d, 32)) != FA_OK) return rc;
+    if (o_dtype == FA_BF16 && 32 % pack == 0 &&
+        (rc = encode_token_map(&p.tm_o, o, d, Tq, Hq, (long long)Hq * d, pack, 32 / pack)) != FA_OK)
+        return rc;
     p.o = o;
-    p.o_sh = d;
-    p.o_sn = (long long)Hq * d;
     p.lse = lse;
     p.B = B;
+    p.Tq = Tq;
     p.Hq = Hq;
     p.Hkv = Hkv;
-    p.Nq = Tq;
-    p.Nk = (int)keys;
     p.R = R;
     p.causal = causal ? 1 : 0;
     p.window = window;
-    p.head_pair = pair ? 1 : 0;
+    p.pack = pack;
+    p.tile_tokens = 128 / pack;
+    p.slots = slots;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.wait_limit_ns = g_wait_limit_ns;
-    p.slots = slots;
-    p.slots_per_group = pair ? R / 2 : R;
-    long long pool_keys = c.paged ? (long long)c.page_size * c.num_pages : keys;
-    if (c.paged && pool_keys > keys * B) pool_keys = keys * B;
-    long long groups = pool_keys > 0 ? kSectionBytes / (pool_keys * d * 4) : Hkv;
-    groups = groups < 1 ? 1 : groups > Hkv ? Hkv : groups;
-    p.section_slots = (int)groups * p.slots_per_group;
     p.plan_head = static_cast<int *>(workspace);
     int4 *plan = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + kVarlenHeadBytes);
     p.plan = plan;
@@ -702,10 +718,18 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     m.B = B;
     m.Tq = Tq;
     m.Tk = (int)keys;
-    m.rows = pair ? 128 : 256;
+    m.rows = 2 * p.tile_tokens;
     m.causal = p.causal;
     m.window = window;
-    m.max_jobs = Tq / m.rows + B;
+    // The variant for a few tokens against many keys -- many tiles without a partner, and units
+    // that are few and long -- judged by the averages, the lengths being known on the device only.
+    // Measured on B200 (32 + 8 heads, d = 128): 12 chunks of 1 to 512 tokens over contexts of up to
+    // 8192 165 us, 175 without it; 512 prompts of 64 tokens (no long context) 176 us against 163.
+    const long long pool_keys = c.paged ? (long long)c.page_size * c.num_pages : keys;
+    const long long all_keys = c.paged && pool_keys > keys * B ? keys * B : pool_keys;
+    const bool few = (long long)Tq <= 4LL * B * p.tile_tokens && all_keys >= 1024LL * B;
+    m.twins = few ? 1 : 0;
+    m.max_jobs = varlen_max_jobs(B, Tq, pack);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     fa::fa_varlen_plan_kernel<<<1, fa::varlen::kThreads, 0, st>>>(m);
     cudaError_t e = cudaGetLastError();
@@ -713,8 +737,8 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     const long long bound = (long long)m.max_jobs * slots;
     const int grid = bound < info->num_sms ? (int)bound : info->num_sms;
     const bool f32 = o_dtype == FA_F32;
-    rc = c.paged ? launch_varlen_variant<fa::kPaged>(p, d, f32, grid, info, st)
-                 : launch_varlen_variant<fa::kPacked>(p, d, f32, grid, info, st);
+    rc = c.paged ? launch_varlen_variant<true>(p, d, f32, few, grid, info, st)
+                 : launch_varlen_variant<false>(p, d, f32, few, grid, info, st);
     if (rc != FA_OK) return rc;
     return ok();
 }
@@ -1103,7 +1127,7 @@ int fa_decode_noalloc(const void *q, const void *kcache, const void *vcache, con
 
 // ---------------------------------------------- rotary positions and cache filling
 
-size_t fa_fwd_varlen_workspace_size(int B, int Tq) { return varlen_ws_bytes(B, Tq); }
+size_t fa_fwd_varlen_workspace_size(int B, int Tq, int Hq, int Hkv) { return varlen_ws_bytes(B, Tq, Hq, Hkv); }
 
 int fa_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q, const int *cu_k,
                   int B, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride, long long k_stride,

@@ -73,22 +73,7 @@ struct PrefillParams {
     int selftest_no_s_signal;  // timeout self-test: never signal a ready score tile
     const float *q_scale, *k_scale, *v_scale;  // FP8 variant: per-head dequantization scales
     long long debug_lse_offset;  // debug builds' bounds self-test: added to every LSE index (else 0)
-    // packed sequences (fa_varlen_plan_kernel writes the plan; Nq and Nk above are then the
-    // rows of the packed q and k)
-    const int4 *plan;        // two per job: {q row of the sequence, Nq, k row, Nk}, {first row, sequence, -, -}
-    int *plan_head;          // [0] number of jobs, [1] units handed out so far
-    int slots;               // head slots: head pairs or heads
-    int section_slots;       // head slots worked on at a time
-    int slots_per_group;     // head slots of one K/V head
-    // packed sequences over pages: tm_k and tm_v are (d, page_size, num_pages * Hkv)
-    const int *block_table;  // (B, max_pages)
-    int page_size, max_pages, num_pages;
-    int box_rows;            // rows per copy: a power of two <= 128 that divides page_size
 };
-
-// The layouts of q, k and v: dense batches (4-D maps), packed sequences, and packed queries
-// over a paged cache.
-enum : int { kDense = 0, kPacked = 1, kPaged = 2 };
 
 namespace prefill {
 
@@ -106,12 +91,6 @@ constexpr float kLazyThreshold = 16.0f;  // log2 units: rescale only past a fact
 constexpr float kLazyThresholdF16 = 8.0f;  // FP8 variant: P <= 2^8 must fit fp16
 constexpr float kLn2 = 0.6931471805599453f;
 
-// A packed unit as the producer hands it to the other roles.
-constexpr int kRecords = 4;
-struct Record {
-    int valid, q_row, nq, nk, h[2], r[2], a[2], n[2];  // [2]: by Q tile
-};
-
 template <int D, bool FP8 = false>
 struct Cfg {
     static constexpr int kTileBytes = 128 * D * 2;             // a 16-bit 128-row tile
@@ -127,11 +106,10 @@ struct Cfg {
     static constexpr int kBarOff = kV16Off + (FP8 ? 2 * kTileBytes : 0);
     // barriers: kv_full[S], kv_empty[S], q_full[2 sets][2], q_empty[2 sets][2], s_full[2],
     //           p_ready[2], o_done[2], o_free[2], teardown, p_half[2]; FP8: v16_full[2],
-    //           v16_empty[2]; packed: rec_full[kRecords]
-    static constexpr int kNumBars = 2 * kStages + 19 + 4;
+    //           v16_empty[2]
+    static constexpr int kNumBars = 2 * kStages + 19 + (FP8 ? 4 : 0);
     static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-    static constexpr int kRecOff = kMiscOff + 64;
-    static constexpr int kSmemBytes = kRecOff + kRecords * (int)sizeof(Record) + 1024;  // + alignment slack
+    static constexpr int kSmemBytes = kMiscOff + 64 + 1024;  // + alignment slack
 };
 
 // A unit: two 128-row Q tiles (s = 0, 1) of one K/V group; tile s reads key tiles
@@ -139,7 +117,6 @@ struct Cfg {
 // one of the two.
 struct Unit {
     int b, g, h0, h1, r0, r1, a0, a1, n0, n1;
-    int q_row, k_row, nq, nk;  // packed: where the sequence's rows begin and how many they are
 };
 
 // Work is dealt out in slots.  A slot belongs to one "head slot" (a head pair of one
@@ -214,79 +191,6 @@ __device__ __forceinline__ int next_unit(const PrefillParams &p, int u, Unit &w)
         if ((u & 1) < units_in_slot(p) && decode_unit<WINDOW>(p, u >> 1, u & 1, w)) return u;
     return -1;
 }
-
-// Packed sequences: unit `u` is one head slot of one job (a row tile, or a pair of them, of one
-// sequence).  The jobs lie in the plan in order of falling cost; units run through the jobs of
-// one section of head slots (whose K and V stay in L2 together), each job with all the
-// section's slots, then through the next section's.
-__device__ __forceinline__ int packed_job(const PrefillParams &p, int n_jobs, int u, int &slot)
-{
-    const int per = n_jobs * p.section_slots;
-    const int sec = u / per;
-    const int rest = u - sec * per;
-    const int here = min(p.section_slots, p.slots - sec * p.section_slots);
-    const int job = rest / here;
-    slot = sec * p.section_slots + rest - job * here;
-    return job;
-}
-
-// The unit of head slot `slot` and the plan's entry (x, y).  A tile whose rows see no key at all
-// (more causal queries than keys, or no keys) still reads one key tile, wholly masked.
-__device__ __forceinline__ void packed_unit(const PrefillParams &p, const int4 &x, const int4 &y, int slot, Unit &w)
-{
-    w.q_row = x.x;
-    w.nq = x.y;
-    w.k_row = x.z;
-    w.nk = x.w;
-    w.b = y.y;
-    w.g = slot / p.slots_per_group;
-    if (p.head_pair) {
-        w.h0 = w.g * p.R + 2 * (slot - w.g * p.slots_per_group);
-        w.h1 = w.h0 + 1;
-        w.r0 = w.r1 = y.x;
-    } else {
-        w.h0 = w.h1 = slot;
-        w.r0 = y.x;
-        w.r1 = w.r0 + BM;
-    }
-    const int nkt = max(1, (w.nk + BN - 1) / BN);
-    w.a0 = w.a1 = 0;
-    w.n0 = w.n1 = nkt;
-    if (p.causal) {
-        const int delta = w.nk - w.nq;
-        w.n0 = min(nkt, max(0, w.r0 + BM - 1 + delta) / BN + 1);
-        w.n1 = min(nkt, max(0, w.r1 + BM - 1 + delta) / BN + 1);
-        if (p.window > 0) {
-            w.a0 = min(w.n0 - 1, max(0, w.r0 + delta - p.window + 1) / BN);
-            w.a1 = min(w.n1 - 1, max(0, w.r1 + delta - p.window + 1) / BN);
-        }
-    }
-    if (w.r1 >= w.nq) {  // a second tile without rows reads one key tile only
-        w.n1 = w.n0;
-        w.a1 = w.n0 - 1;
-    }
-}
-
-// Clear rows [first, 128) of a V tile (all slabs; the swizzle permutes within a row), so that
-// what lies behind a sequence's last key -- another sequence's rows, or whatever a page holds
-// there, NaN and infinities included -- meets the weights 0 as zeros.  Whole warp.
-template <int D>
-__device__ __forceinline__ void clear_v_rows(uint8_t *tile, int first, int lane)
-{
-    const int n = (BN - first) * 8;  // 16-byte chunks of one slab
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-        uint4 *at = reinterpret_cast<uint4 *>(tile + c * kChunkBytes + first * 128);
-        for (int i = lane; i < n; i += 32) at[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    ptx::fence_proxy_async_smem();  // the tensor core reads these through the async proxy
-    __syncwarp();
-}
-
-// A value that all lanes hold, as one the compiler knows to be the same in all of them: the
-// MMA warp's loop bounds, and all that follows from them, then stay in uniform registers (from
-// plain loads of the record they took vector registers, 190 bytes of spills in that warp).
-__device__ __forceinline__ int warp_uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // S = Q K^T over the full head dimension: D/16 MMAs of K = 16.  Both operands are
 // K-major 128-byte-swizzled tiles: 8-row groups 1024 bytes apart (stride offset), a
@@ -475,18 +379,14 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity, uint6
 
 // SPLIT_P: hand P to the MMA warp in two halves (used for head-pair units; measured to
 // help the grouped-query tiling and to cost a little on the row-pair tiling).  FP8: Q, K
-// and V in E4M3 (d = 128 only).  LAYOUT: dense batches; or packed sequences (kPacked, kPaged),
-// whose units the producer draws from a counter -- lengths differ, so no fixed deal of the
-// units balances -- and hands to the other roles through a ring of records in shared memory.
-template <int D, bool OUT_F32, bool SPLIT_P, bool WINDOW, bool FP8 = false, int LAYOUT = kDense>
+// and V in E4M3 (d = 128 only).
+template <int D, bool OUT_F32, bool SPLIT_P, bool WINDOW, bool FP8 = false>
 __global__ void __launch_bounds__(prefill::kThreads, 1)
     fa_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
     using namespace prefill;
     using C = Cfg<D, FP8>;
     static_assert(!FP8 || D == 128, "FP8 prefill: head dim 128");
-    constexpr bool PACK = LAYOUT != kDense;
-    static_assert(!PACK || (WINDOW && !FP8), "packed units carry their window; no FP8");
     constexpr int kBoxes = FP8 ? 1 : D / 64;  // 128-byte column boxes per loaded tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -505,8 +405,6 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
     uint64_t *p_half = q_full + 17;     // [2]: first 64 keys of P_s written
     uint64_t *v16_full = q_full + 19;   // FP8 [2]: widened V tile written (one arrive per widening warp)
     uint64_t *v16_empty = q_full + 21;  // FP8 [2]: widened V tile read by its last P V
-    uint64_t *rec_full = q_full + 19;   // packed [kRecords]: a unit's record written
-    volatile Record *records = reinterpret_cast<volatile Record *>(smem + C::kRecOff);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::kMiscOff);
     int *stop_flag = reinterpret_cast<int *>(smem + C::kMiscOff + 4);
 
@@ -539,8 +437,6 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
             ptx::mbar_init(&o_done[s], 1);
             ptx::mbar_init(&o_free[s], 128);
         }
-        if (PACK)
-            for (int i = 0; i < kRecords; ++i) ptx::mbar_init(&rec_full[i], 1);
         ptx::mbar_init(teardown, 1);
         *stop_flag = 0;
         ptx::fence_barrier_init();
@@ -559,11 +455,6 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     const StopFlag sf{stop_flag, p.wait_limit_ns};
-    // packed: unit number i of this CTA's order has a record (false at the end)
-    auto have_record = [&](uint32_t i) -> bool {
-        if (!wait_warp(&rec_full[i % kRecords], (i / kRecords) & 1u, sf)) return false;
-        return __any_sync(0xffffffffu, records[i % kRecords].valid);
-    };
 
     const uint32_t q_saddr0 = ptx::smem_addr(smem + C::kQOff);
     const uint32_t kv_saddr0 = ptx::smem_addr(smem + C::kKVOff);
@@ -588,181 +479,54 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
             if (leader) {
                 ptx::mbar_arrive_expect_tx(&q_full[qi], C::kInTileBytes);
                 const int h = s ? uw.h1 : uw.h0;
-                const int r = (PACK ? uw.q_row : 0) + (s ? uw.r1 : uw.r0);
+                const int r = s ? uw.r1 : uw.r0;
                 uint8_t *dst = smem + C::kQOff + qi * C::kInTileBytes;
 #pragma unroll
                 for (int c = 0; c < kBoxes; ++c)
-                    ptx::tma_load_4d(dst + c * kChunkBytes, &p.tm_q, &q_full[qi], 64 * c, r, h, PACK ? 0 : uw.b);
+                    ptx::tma_load_4d(dst + c * kChunkBytes, &p.tm_q, &q_full[qi], 64 * c, r, h, uw.b);
             }
             __syncwarp();
         };
         auto q_slot = [&](uint32_t i, int s) { return &q_empty[2 * (int)(i & 1u) + s]; };
         auto q_free_parity = [&](uint32_t i) { return ((i >> 1) & 1u) ^ 1u; };
-        if constexpr (PACK) {
-            // Unit 0 is the CTA's own number, the others come from the counter.  At the start of
-            // unit i the number of unit i + 1 is known and that of i + 2 is asked for, so neither
-            // the counter's nor the plan's latency holds up the K/V stream.
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is complete
-            const int n_jobs = __ldcg(&p.plan_head[0]);
-            const int n_units = n_jobs * p.slots;
-            auto draw = [&]() { return leader ? (int)gridDim.x + atomicAdd(&p.plan_head[1], 1) : 0; };
-            const int src_lane = __ffs(__ballot_sync(0xffffffffu, leader)) - 1;
-            auto publish = [&](uint32_t i, bool valid, const Unit &uw) {
-                if (leader) {
-                    volatile Record &r = records[i % kRecords];
-                    r.valid = valid ? 1 : 0;
-                    if (valid) {
-                        r.q_row = uw.q_row;
-                        r.nq = uw.nq;
-                        r.nk = uw.nk;
-                        r.h[0] = uw.h0;
-                        r.h[1] = uw.h1;
-                        r.r[0] = uw.r0;
-                        r.r[1] = uw.r1;
-                        r.a[0] = uw.a0;
-                        r.a[1] = uw.a1;
-                        r.n[0] = uw.n0;
-                        r.n[1] = uw.n1;
-                    }
-                    ptx::mbar_arrive(&rec_full[i % kRecords]);
-                }
-                __syncwarp();
-            };
-            // Pages: lane l looks up the page of copy l of a key tile (box_rows keys), one tile
-            // ahead of its use.  Keys past the end, and pages outside the pool (reported), read
-            // the plane behind the last, which the copy engine fills with zeros.
-            const int boxes = LAYOUT == kPaged ? BN / p.box_rows : 1;
-            constexpr int kNoPage = -0x40000000;
-            auto page_of = [&](const Unit &uw, int j) -> int {
-                const int pos = BN * j + lane * p.box_rows;
-                if (lane >= boxes || pos >= uw.nk) return kNoPage;
-                const long long at = (long long)uw.b * p.max_pages + pos / p.page_size;
-                return in_bounds(at, (long long)p.B * p.max_pages) ? p.block_table[at] : kNoPage;
-            };
-            auto plane_of = [&](int pg, int g) -> int {
-                if (pg >= 0 && pg < p.num_pages) return pg * p.Hkv + g;
-                if (pg != kNoPage) raise_error(kErrPageRange);
-                return p.num_pages * p.Hkv;
-            };
-            Unit w, wn;
-            int slot = 0, u = (int)blockIdx.x;
-            int next_raw = draw();
-            uint32_t i = 0;
-            bool have = u < n_units;
-            if (have) {
-                const int job = packed_job(p, n_jobs, u, slot);
-                packed_unit(p, __ldcg(&p.plan[2 * job]), __ldcg(&p.plan[2 * job + 1]), slot, w);
-            }
-            publish(0, have, w);
-            for (int s = 0; ok && have && s < 2; ++s) {
-                if (!wait_warp(q_slot(0, s), q_free_parity(0), sf)) ok = false;
-                else issue_q(w, 0, s);
-            }
-            int page = (LAYOUT == kPaged && have) ? page_of(w, w.a0) : 0;
-            int page_n = 0;  // of the next unit's first tile
-            for (; ok && have; ++i) {
-                u = __shfl_sync(0xffffffffu, next_raw, src_lane);
-                const bool have_n = u < n_units;
-                if (have_n) next_raw = draw();
-                int4 px = make_int4(0, 0, 0, 0), py = px;  // the next unit's plan entry, in flight
-                int slot_n = 0;
-                if (have_n) {
-                    const int job = packed_job(p, n_jobs, u, slot_n);
-                    px = __ldcg(&p.plan[2 * job]);
-                    py = __ldcg(&p.plan[2 * job + 1]);
-                }
-                bool told = false;
-                auto tell = [&]() {
-                    if (have_n) packed_unit(p, px, py, slot_n, wn);
-                    if (LAYOUT == kPaged && have_n) page_n = page_of(wn, wn.a0);
-                    publish(i + 1, have_n, wn);
-                    told = true;
-                };
-                int q_next = have_n ? 0 : 2;  // look-ahead Q tiles already issued
-                for (int j = w.a0; j < w.n1 && ok; ++j) {
-                    const int plane = LAYOUT == kPaged ? plane_of(page, w.g) : 0;
-                    if (LAYOUT == kPaged && j + 1 < w.n1) page = page_of(w, j + 1);
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t st = kv_it % C::kStages;
-                        const uint32_t ph = (kv_it / C::kStages) & 1u;
-                        if (!wait_warp(&kv_empty[st], ph ^ 1u, sf)) { ok = false; break; }
+        Unit w, wn;
+        int u = next_unit<WINDOW>(p, 2 * (int)blockIdx.x, w);
+        uint32_t i = 0;
+        for (int s = 0; ok && u >= 0 && s < 2; ++s) {
+            if (!wait_warp(q_slot(0, s), q_free_parity(0), sf)) ok = false;
+            else issue_q(w, 0, s);
+        }
+        for (; ok && u >= 0; ++i) {
+            const int un = next_unit<WINDOW>(p, unit_step(u), wn);
+            int q_next = (un >= 0) ? 0 : 2;  // look-ahead Q tiles already issued
+            for (int j = w.a0; j < w.n1 && ok; ++j) {
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t st = kv_it % C::kStages;
+                    const uint32_t ph = (kv_it / C::kStages) & 1u;
+                    if (!wait_warp(&kv_empty[st], ph ^ 1u, sf)) { ok = false; break; }
+                    if (leader) {
+                        ptx::mbar_arrive_expect_tx(&kv_full[st], C::kInTileBytes);
                         uint8_t *dst = smem + C::kKVOff + st * C::kInTileBytes;
                         const CUtensorMap *map = kv ? &p.tm_v : &p.tm_k;
-                        if (leader) {
-                            ptx::mbar_arrive_expect_tx(&kv_full[st], C::kInTileBytes);
-                            if (LAYOUT == kPacked) {
 #pragma unroll
-                                for (int c = 0; c < kBoxes; ++c)
-                                    ptx::tma_load_4d(dst + c * kChunkBytes, map, &kv_full[st], 64 * c,
-                                                     w.k_row + BN * j, w.g, 0);
-                            }
-                        }
-                        __syncwarp();
-                        if (LAYOUT == kPaged && lane < boxes) {
-                            const int pos = BN * j + lane * p.box_rows;
-#pragma unroll
-                            for (int c = 0; c < kBoxes; ++c)
-                                ptx::tma_load_3d(dst + c * kChunkBytes + lane * p.box_rows * 128, map, &kv_full[st],
-                                                 64 * c, pos % p.page_size, plane);
-                        }
-                        __syncwarp();
-                        ++kv_it;
-                        if (kv == 1 && !told) tell();
-                        while (told && q_next < 2 &&
-                               __all_sync(0xffffffffu, ptx::mbar_test(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
-                            issue_q(wn, i + 1, q_next);
-                            ++q_next;
-                        }
+                        for (int c = 0; c < kBoxes; ++c)
+                            ptx::tma_load_4d(dst + c * kChunkBytes, map, &kv_full[st], 64 * c, BN * j, w.g, w.b);
+                    }
+                    __syncwarp();
+                    ++kv_it;
+                    while (q_next < 2 &&
+                           __all_sync(0xffffffffu, ptx::mbar_test(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
+                        issue_q(wn, i + 1, q_next);
+                        ++q_next;
                     }
                 }
-                for (; ok && q_next < 2; ++q_next) {
-                    if (!wait_warp(q_slot(i + 1, q_next), q_free_parity(i + 1), sf)) ok = false;
-                    else issue_q(wn, i + 1, q_next);
-                }
-                have = have_n;
-                w = wn;
-                page = page_n;
             }
-        } else {
-            Unit w, wn;
-            int u = next_unit<WINDOW>(p, 2 * (int)blockIdx.x, w);
-            uint32_t i = 0;
-            for (int s = 0; ok && u >= 0 && s < 2; ++s) {
-                if (!wait_warp(q_slot(0, s), q_free_parity(0), sf)) ok = false;
-                else issue_q(w, 0, s);
+            for (; ok && q_next < 2; ++q_next) {
+                if (!wait_warp(q_slot(i + 1, q_next), q_free_parity(i + 1), sf)) ok = false;
+                else issue_q(wn, i + 1, q_next);
             }
-            for (; ok && u >= 0; ++i) {
-                const int un = next_unit<WINDOW>(p, unit_step(u), wn);
-                int q_next = (un >= 0) ? 0 : 2;  // look-ahead Q tiles already issued
-                for (int j = w.a0; j < w.n1 && ok; ++j) {
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const uint32_t st = kv_it % C::kStages;
-                        const uint32_t ph = (kv_it / C::kStages) & 1u;
-                        if (!wait_warp(&kv_empty[st], ph ^ 1u, sf)) { ok = false; break; }
-                        if (leader) {
-                            ptx::mbar_arrive_expect_tx(&kv_full[st], C::kInTileBytes);
-                            uint8_t *dst = smem + C::kKVOff + st * C::kInTileBytes;
-                            const CUtensorMap *map = kv ? &p.tm_v : &p.tm_k;
-#pragma unroll
-                            for (int c = 0; c < kBoxes; ++c)
-                                ptx::tma_load_4d(dst + c * kChunkBytes, map, &kv_full[st], 64 * c, BN * j, w.g, w.b);
-                        }
-                        __syncwarp();
-                        ++kv_it;
-                        while (q_next < 2 &&
-                               __all_sync(0xffffffffu, ptx::mbar_test(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
-                            issue_q(wn, i + 1, q_next);
-                            ++q_next;
-                        }
-                    }
-                }
-                for (; ok && q_next < 2; ++q_next) {
-                    if (!wait_warp(q_slot(i + 1, q_next), q_free_parity(i + 1), sf)) ok = false;
-                    else issue_q(wn, i + 1, q_next);
-                }
-                u = un;
-                w = wn;
-            }
+            u = un;
+            w = wn;
         }
         // Let every copy this warp started land before the CTA can exit.
         if (leader) {
@@ -826,17 +590,7 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
             return true;
         };
         Unit w;
-        for (int u = PACK ? 0 : next_unit<WINDOW>(p, 2 * (int)blockIdx.x, w); ok && u >= 0;
-             u = PACK ? 0 : next_unit<WINDOW>(p, unit_step(u), w)) {
-            if constexpr (PACK) {
-                if (!have_record(units)) break;
-                const volatile Record &r = records[units % kRecords];
-                w.nk = warp_uniform(r.nk);
-                w.a0 = warp_uniform(r.a[0]);
-                w.a1 = warp_uniform(r.a[1]);
-                w.n0 = warp_uniform(r.n[0]);
-                w.n1 = warp_uniform(r.n[1]);
-            }
+        for (int u = next_unit<WINDOW>(p, 2 * (int)blockIdx.x, w); ok && u >= 0; u = next_unit<WINDOW>(p, unit_step(u), w)) {
             const uint32_t free_par = (units & 1u) ^ 1u;  // first unit passes at once
             const uint32_t qset = units & 1u;
             const uint32_t q_par = (units >> 1) & 1u;
@@ -884,8 +638,6 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
                 }
                 __syncwarp();
                 if (!wait_warp(v_ready, vph, sf)) { ok = false; break; }
-                if (PACK && BN * j + BN > w.nk)
-                    clear_v_rows<D>(smem + C::kKVOff + vs * C::kInTileBytes, max(0, w.nk - BN * j), lane);
                 if (j < w.n0) {
                     if (!issue_pv_halves(0, vs, j > w.a0, j == w.a0, free_par)) { ok = false; break; }
                     if (leader && j == w.n0 - 1) ptx::mma_commit(&o_done[0]);
@@ -925,30 +677,14 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
         float sl2 = p.scale_log2;
         uint32_t s_ph = 0, units = 0;
         Unit w;
-        for (int u = PACK ? 0 : next_unit<WINDOW>(p, 2 * (int)blockIdx.x, w); u >= 0;
-             u = PACK ? 0 : next_unit<WINDOW>(p, unit_step(u), w)) {
-            // Packed: what the key loop needs is read from the record here, what the epilogue
-            // needs there (the record stays in place until this unit's last role is done), so
-            // that it takes no registers in between.
-            const volatile Record &rec = records[PACK ? units % kRecords : 0];
-            if (PACK && !have_record(units)) break;
-            int h = 0, r0 = 0, row = 0, a, n, lim, first = 0;
-            if constexpr (PACK) {
-                const int nk = rec.nk;
-                const int diag = rec.r[s] + tid + (nk - rec.nq);  // last key of a causal row
-                a = rec.a[s];
-                n = rec.n[s];
-                lim = p.causal ? min(diag, nk - 1) : nk - 1;
-                if (p.window > 0) first = diag - p.window + 1;
-            } else {
-                h = s ? w.h1 : w.h0;
-                r0 = s ? w.r1 : w.r0;
-                a = s ? w.a1 : w.a0;
-                n = s ? w.n1 : w.n0;
-                row = r0 + tid;
-                lim = p.causal ? min(row + (p.Nk - p.Nq), p.Nk - 1) : p.Nk - 1;
-                first = WINDOW ? row + (p.Nk - p.Nq) - p.window + 1 : 0;
-            }
+        for (int u = next_unit<WINDOW>(p, 2 * (int)blockIdx.x, w); u >= 0; u = next_unit<WINDOW>(p, unit_step(u), w)) {
+            const int h = s ? w.h1 : w.h0;
+            const int r0 = s ? w.r1 : w.r0;
+            const int a = s ? w.a1 : w.a0;
+            const int n = s ? w.n1 : w.n0;
+            const int row = r0 + tid;
+            const int lim = p.causal ? min(row + (p.Nk - p.Nq), p.Nk - 1) : p.Nk - 1;
+            const int first = WINDOW ? row + (p.Nk - p.Nq) - p.window + 1 : 0;
             // FP8: the scores are products of E4M3 codes; the head scales join the softmax scale
             if (FP8) {
                 const bool okq = in_bounds(h, p.Hq), okk = in_bounds(w.g, p.Hkv);
@@ -1043,22 +779,10 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
             // warp waits for another.  fp32 output is stored row by row.
             if (!wait_warp(&o_done[s], units & 1u, sf)) break;
             ptx::tc_fence_after();
-            int nq = p.Nq, q_row = 0;
-            if constexpr (PACK) {
-                nq = rec.nq;
-                q_row = rec.q_row;
-                h = rec.h[s];
-                r0 = rec.r[s];
-                row = r0 + tid;
-            }
-            const bool valid = row < nq;
+            const bool valid = row < p.Nq;
             // FP8: the widened V holds the E4M3 codes; v_scale restores V
-            const float inv_l = FP8              ? (in_bounds(w.g, p.Hkv) ? p.v_scale[w.g] : 1.f) / lo
-                                : (PACK && lo == 0.f) ? 0.f
-                                                      : 1.f / lo;
-            // LSE index
-            long long orow = PACK ? (long long)h * p.Nq + q_row + (valid ? row : 0)
-                                  : ((long long)w.b * p.Hq + h) * (long long)p.Nq + (valid ? row : 0);
+            const float inv_l = FP8 ? (in_bounds(w.g, p.Hkv) ? p.v_scale[w.g] : 1.f) / lo : 1.f / lo;
+            long long orow = ((long long)w.b * p.Hq + h) * (long long)p.Nq + (valid ? row : 0);  // LSE index
             if (kDebugChecks) orow += p.debug_lse_offset;
             const int qi = 2 * (int)(units & 1u) + s;
             uint32_t ov[D];
@@ -1067,13 +791,8 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
             ptx::tmem_wait_ld();
             ptx::tc_fence_before();
             ptx::mbar_arrive(&o_free[s]);
-            if (PACK && lo == 0.f) {  // the row sees no key: O = 0 (and the LSE below is -inf)
-#pragma unroll
-                for (int e = 0; e < D; ++e) ov[e] = 0u;
-            }
             if (OUT_F32) {
-                const long long ooff = PACK ? h * p.o_sh + (q_row + (long long)row) * p.o_sn
-                                            : w.b * p.o_sb + h * p.o_sh + (long long)row * p.o_sn;
+                const long long ooff = w.b * p.o_sb + h * p.o_sh + (long long)row * p.o_sn;
                 if (valid && in_bounds(ooff + D - 1, (long long)p.B * p.Hq * p.Nq * D)) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + ooff);
 #pragma unroll
@@ -1113,8 +832,6 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(&q_empty[qi]);
             } else {
                 uint8_t *stage = smem + C::kQOff + qi * C::kTileBytes;
-                const bool by_row = PACK && r0 + 32 * (warp & 3) + 32 > nq;  // (warp-uniform)
-                const long long ooff = PACK ? h * p.o_sh + (q_row + (long long)row) * p.o_sn : 0;
 #pragma unroll
                 for (int e = 0; e < D / 8; ++e) {
                     uint4 v4;
@@ -1124,29 +841,23 @@ __global__ void __launch_bounds__(prefill::kThreads, 1)
                     v4.w = ptx::pack_bf16x2(__uint_as_float(ov[8 * e + 6]) * inv_l, __uint_as_float(ov[8 * e + 7]) * inv_l);
                     // 16-byte chunk e of the row: slab e / 8, chunk (e % 8) swizzled by row % 8
                     const int slab = e >> 3, chunk = (e & 7) ^ (tid & 7);
-                    if (!by_row)
-                        *reinterpret_cast<uint4 *>(stage + slab * kChunkBytes + tid * 128 + chunk * 16) = v4;
-                    else if (valid && in_bounds(ooff + D - 1, (long long)p.Hq * p.Nq * D))
-                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + ooff + 8 * e) = v4;
+                    *reinterpret_cast<uint4 *>(stage + slab * kChunkBytes + tid * 128 + chunk * 16) = v4;
                 }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     const int wr = 32 * (warp & 3);  // this warp's rows of the tile
-                    // (rows past Nq are never stored: the map ends there, or -- packed -- a warp
-                    // whose rows pass the sequence's end stores them one by one below)
-                    if ((PACK ? r0 + wr + 32 <= nq : r0 + wr < p.Nq && in_bounds(w.b, p.B)) && in_bounds(h, p.Hq)) {
+                    if (r0 + wr < p.Nq && in_bounds(h, p.Hq) && in_bounds(w.b, p.B)) {  // (rows past Nq are never stored)
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
-                            ptx::tma_store_4d(&p.tm_o, stage + c * kChunkBytes + wr * 128, 64 * c,
-                                              q_row + r0 + wr, h, PACK ? 0 : w.b);
+                            ptx::tma_store_4d(&p.tm_o, stage + c * kChunkBytes + wr * 128, 64 * c, r0 + wr, h, w.b);
                         ptx::bulk_commit_group();
                         ptx::bulk_wait_group_read0();
                     }
                     ptx::mbar_arrive(&q_empty[qi]);
                 }
             }
-            if (valid && in_bounds(orow, (long long)(PACK ? 1 : p.B) * p.Hq * p.Nq)) p.lse[orow] = (m + ptx::lg2(l)) * kLn2;
+            if (valid && in_bounds(orow, (long long)p.B * p.Hq * p.Nq)) p.lse[orow] = (m + ptx::lg2(l)) * kLn2;
             ++units;
         }
         if (!OUT_F32 && lane == 0) ptx::bulk_wait_group0();  // stores complete before exit

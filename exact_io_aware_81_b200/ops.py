@@ -49,7 +49,7 @@ SIGNATURES = {
     "fa_decode_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _Z, _P]),
     "fa_decode_paged_fp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                  _P, _Z, _P]),
-    "fa_fwd_varlen_workspace_size": (_Z, [_I, _I]),
+    "fa_fwd_varlen_workspace_size": (_Z, [_I] * 4),
     "fa_fwd_varlen": (_I, [_P] * 7 + [_I] * 6 + [_L] * 3 + [_F, _I, _I, _I, _P, _Z, _P]),
     "fa_fwd_varlen_paged": (_I, [_P] * 8 + [_I] * 8 + [_L, _F, _I, _I, _I, _P, _Z, _P]),
     "fa_rope": (_I, [_P] * 7 + [_I] * 6 + [_L] * 4 + [_I] * 3 + [_P]),
@@ -571,8 +571,8 @@ _ROPE_TYPES = (torch.bfloat16, torch.float32)
 _BF16 = (torch.bfloat16,)
 
 
-def varlen_workspace_size(B: int, Tq: int) -> int:
-    return int(load().fa_fwd_varlen_workspace_size(B, Tq))
+def varlen_workspace_size(B: int, Tq: int, Hq: int, Hkv: int) -> int:
+    return int(load().fa_fwd_varlen_workspace_size(B, Tq, Hq, Hkv))
 
 
 def _varlen_outputs(q, dev, out_dtype, out, lse):
@@ -599,7 +599,7 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     strided or not; cu_seqlens_q / cu_seqlens_k int32 (B+1,) on the device (the latter defaults to
     the former).  Returns (o (Tq,Hq,d), lse fp32 (Hq,Tq)); causal is bottom-right aligned in each
     sequence, a row that sees no key gives o = 0 and lse = -inf.  ``workspace`` is a uint8 CUDA
-    tensor of varlen_workspace_size(B, Tq) bytes; one is allocated if omitted."""
+    tensor of varlen_workspace_size(B, Tq, Hq, Hkv) bytes; one is allocated if omitted."""
     dev = q.device
     pq, sq = _rows(q, "q", _BF16, dev)
     pk, sk = _rows(k, "k", _BF16, dev)
@@ -616,7 +616,7 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
         scale = 1.0 / math.sqrt(d)
     if Tq == 0:
         return out, lse
-    pw, nw, workspace = _scratch(workspace, varlen_workspace_size(B, Tq), dev)
+    pw, nw, workspace = _scratch(workspace, varlen_workspace_size(B, Tq, Hq, Hkv), dev)
     _launch(load().fa_fwd_varlen, dev, stream, pq, pk, pv, po, pl, pcq, pck, B, Tq, Tk, Hq, Hkv, d, sq, sk, sv,
             float(scale), int(bool(causal)), int(window), odt, pw, nw)
     return out, lse
@@ -647,7 +647,7 @@ def fwd_varlen_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
         scale = 1.0 / math.sqrt(d)
     if Tq == 0:
         return out, lse
-    pw, nw, workspace = _scratch(workspace, varlen_workspace_size(B, Tq), dev)
+    pw, nw, workspace = _scratch(workspace, varlen_workspace_size(B, Tq, Hq, Hkv), dev)
     _launch(load().fa_fwd_varlen_paged, dev, stream, pq, pkp, pvp, pbt, pcq, psl, po, pl, B, Tq, Hq, Hkv, num_pages,
             page_size, max_pages, d, sq, float(scale), int(bool(causal)), int(window), odt, pw, nw)
     return out, lse

@@ -292,11 +292,11 @@ FA_API int fa_decode_noalloc(const void *q, const void *kcache, const void *vcac
  *             key (also m = 0) gets o = 0, lse = -inf.  Sequences without rows are skipped.
  * Rows of o and lse that belong to no sequence are left as they were.  Nothing of one sequence
  * (NaN and infinities included) reaches another.
- *   workspace: device scratch of fa_fwd_varlen_workspace_size(B, Tq) bytes, 16-byte aligned,
+ *   workspace: device scratch of fa_fwd_varlen_workspace_size(B, Tq, Hq, Hkv) bytes, 16-byte aligned,
  *             contents ignored and overwritten; calls that share it must be ordered.
  * Supported: d in {64, 128}, B <= 4096, Tq < 2^26, Tk < 2^30 (FA_ERR_UNSUPPORTED otherwise).
  */
-FA_API size_t fa_fwd_varlen_workspace_size(int B, int Tq);
+FA_API size_t fa_fwd_varlen_workspace_size(int B, int Tq, int Hq, int Hkv);
 FA_API int fa_fwd_varlen(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_q,
                          const int *cu_k, int B, int Tq, int Tk, int Hq, int Hkv, int d, long long q_stride,
                          long long k_stride, long long v_stride, float scale, int causal, int window, int o_dtype,

@@ -32,7 +32,7 @@ def run(q, k, v, cq, ck, causal, window=0, out_dtype=torch.bfloat16, scale=None)
     lbuf, lse = guarded((Hq, Tq), torch.float32, DEV)
     o.fill_(SENTINEL)
     lse.fill_(SENTINEL)
-    ws = torch.full((ops.varlen_workspace_size(cq.numel() - 1, Tq),), 0xFF, dtype=torch.uint8, device=DEV)
+    ws = torch.full((ops.varlen_workspace_size(cq.numel() - 1, Tq, Hq, k.shape[1]),), 0xFF, dtype=torch.uint8, device=DEV)
     ops.fwd_varlen(q.to(DEV), k.to(DEV), v.to(DEV), cq.to(DEV), ck.to(DEV) if ck is not None else None, causal=causal,
                    window=window, out_dtype=out_dtype, scale=scale, workspace=ws, out=o, lse=lse)
     status = ops.get_error()
@@ -60,7 +60,7 @@ LENGTHS = [
     [129, 127, 128, 255, 257, 3],
     [700, 1, 2, 400],
 ]
-HEADS = [(4, 2, 128), (8, 8, 64), (6, 2, 64), (8, 1, 128), (3, 1, 128), (2, 2, 128)]
+HEADS = [(4, 2, 128), (8, 8, 64), (6, 2, 64), (8, 1, 128), (3, 1, 128), (2, 2, 128), (32, 1, 64), (40, 1, 128), (10, 2, 64)]
 
 
 @pytest.mark.parametrize("causal", [True, False])
@@ -99,10 +99,11 @@ def test_fp32_output_and_scale(Hq, Hkv, d):
     verify(o, lse, q, k, v, cu(nq), None, True, scale=0.2)
 
 
-@pytest.mark.parametrize("Hq,Hkv,d,window", [(8, 2, 128, 0), (3, 1, 64, 0), (4, 4, 128, 0), (8, 2, 128, 200)])
-def test_equal_lengths_are_the_dense_call(Hq, Hkv, d, window):
-    """B sequences of one length: the (B, N, H, d) call, bit for bit."""
-    B, N = 3, 333
+@pytest.mark.parametrize("Hq,Hkv,d,window,N", [(8, 2, 128, 0, 320), (3, 1, 64, 0, 336), (4, 4, 128, 0, 512), (8, 2, 128, 200, 320)])
+def test_equal_lengths_are_the_dense_call(Hq, Hkv, d, window, N):
+    """B sequences of one length: the (B, N, H, d) call, bit for bit, where the tokens fill whole
+    pairs of tiles (the tokens left over in one tile take its key tiles in two sums)."""
+    B = 3
     q, k, v = make([N] * B, [N] * B, Hq, Hkv, d, 7)
     o, lse, _ = run(q, k, v, cu([N] * B), None, True, window)
     sh = lambda t: t.to(DEV).view(B, N, *t.shape[1:])  # noqa: E731
@@ -278,7 +279,7 @@ def test_two_streams_with_their_own_workspaces():
     full, fl = ops.fwd_varlen(q, k, v, c, causal=False)
     torch.cuda.synchronize()
     a, b = torch.cuda.Stream(), torch.cuda.Stream()
-    ws = [torch.empty(ops.varlen_workspace_size(len(n), sum(n)), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    ws = [torch.empty(ops.varlen_workspace_size(len(n), sum(n), 8, 2), dtype=torch.uint8, device=DEV) for _ in range(2)]
     outs = []
     torch.cuda.synchronize()
     for _ in range(5):
@@ -294,7 +295,7 @@ def test_captured_and_replayed_with_other_lengths():
     Hq, Hkv, d, T = 8, 2, 128, 600
     q, k, v = (t.to(DEV) for t in make([T], [T], Hq, Hkv, d, 41))
     c = cu([100, 200, 300]).to(DEV)
-    ws = torch.empty(ops.varlen_workspace_size(3, T), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(ops.varlen_workspace_size(3, T, Hq, Hkv), dtype=torch.uint8, device=DEV)
     o, lse = torch.empty_like(q), torch.empty(Hq, T, device=DEV)
     ops.fwd_varlen(q, k, v, c, causal=True, workspace=ws, out=o, lse=lse)
     graph = torch.cuda.CUDAGraph()
