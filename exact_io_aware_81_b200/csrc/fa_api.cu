@@ -763,17 +763,35 @@ bool stride_ok(long long stride, int heads, int d, int elem)
 }
 
 template <int D, typename T, bool PAGES, bool FP8>
-void launch_rope(const fa::RopeParams &p, bool rot, bool vec, int grid, cudaStream_t st)
+void launch_rope(fa::RopeParams &p, bool rot, bool vec, int num_sms, cudaStream_t st)
 {
-    constexpr int threads = 32 * fa::rope::kWarps;
+    using namespace fa::rope;
+    const int rows = p.Hq + p.Hkv + (PAGES ? p.Hkv : 0);
+    if (rot && !vec) {
+        // a warp per token, or per share of a token's rows while warps are few
+        p.split = num_sms * 32 / p.T;
+        p.split = p.split < 1 ? 1 : p.split > rows ? rows : p.split;
+        const long long ctas = ((long long)p.T * p.split + kWarps - 1) / kWarps;
+        const int grid = ctas < num_sms * 8 ? (int)ctas : num_sms * 8;
+        fa::fa_rope_any_kernel<D, T, PAGES, FP8><<<grid, kThreads, 0, st>>>(p);
+        return;
+    }
+    // Tokens per CTA: one while that leaves SMs idle, kTokens from two rounds of CTAs on; with
+    // fewer tokens than SMs a token's rows are shared out, at least one step of rows to a CTA.
+    const int step = kThreads / (D * (int)sizeof(T) / 32);
+    p.tokens = p.T >= num_sms * 2 * kTokens ? kTokens : 1;
+    const int groups = (p.T + p.tokens - 1) / p.tokens;
+    const int most = (p.tokens * rows + step - 1) / step;
+    p.split = num_sms / groups;
+    p.split = p.split < 1 ? 1 : p.split > most ? most : p.split;
+    const long long grid = (long long)groups * p.split;
     if constexpr (PAGES) {
         if (!rot) {
-            fa::fa_rope_kernel<D, T, PAGES, FP8, false, true><<<grid, threads, 0, st>>>(p);
+            fa::fa_rope_kernel<D, T, PAGES, FP8, false><<<(unsigned)grid, kThreads, 0, st>>>(p);
             return;
         }
     }
-    if (vec) fa::fa_rope_kernel<D, T, PAGES, FP8, true, true><<<grid, threads, 0, st>>>(p);
-    else fa::fa_rope_any_kernel<D, T, PAGES, FP8><<<grid, threads, 0, st>>>(p);
+    fa::fa_rope_kernel<D, T, PAGES, FP8, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
 }
 
 // Validation and launch shared by fa_rope (pages null), fa_rope_append and fa_cache_append
@@ -827,32 +845,20 @@ int rope_general(fa::RopeParams &p, const PageDest *pages, int d, int dtype, voi
     DeviceInfo *info;
     if ((rc = current_device(&dev, &info)) != FA_OK) return rc;
 
-    // A warp takes a whole token when there are tokens enough to fill the GPU; with fewer, a
-    // token's rows are shared out, at least one load of rows per warp.
-    const int chunks = d * es / 16, rows_at_once = 64 / chunks;
-    const int rows = p.Hq + p.Hkv + (pages ? p.Hkv : 0);
-    const int max_split = (rows + rows_at_once - 1) / rows_at_once;
-    const int warps = info->num_sms * 32;
-    p.split = warps / p.T;
-    if (p.split > max_split) p.split = max_split;
-    if (p.split < 1) p.split = 1;
-    const long long ctas = ((long long)p.T * p.split + fa::rope::kWarps - 1) / fa::rope::kWarps;
-    const int max_ctas = info->num_sms * 8;
-    const int grid = ctas < max_ctas ? (int)ctas : max_ctas;
     const int per = 16 / es;  // elements per 16-byte chunk
     const bool vec = p.interleaved ? (2 * p.F) % per == 0 : p.F % per == 0;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pages) {
-        if (fp8) launch_rope<128, __nv_bfloat16, true, true>(p, rot, vec, grid, st);
-        else if (d == 128) launch_rope<128, __nv_bfloat16, true, false>(p, rot, vec, grid, st);
-        else launch_rope<64, __nv_bfloat16, true, false>(p, rot, vec, grid, st);
+        if (fp8) launch_rope<128, __nv_bfloat16, true, true>(p, rot, vec, info->num_sms, st);
+        else if (d == 128) launch_rope<128, __nv_bfloat16, true, false>(p, rot, vec, info->num_sms, st);
+        else launch_rope<64, __nv_bfloat16, true, false>(p, rot, vec, info->num_sms, st);
     } else if (dtype == FA_F32) {
-        if (d == 128) launch_rope<128, float, false, false>(p, true, vec, grid, st);
-        else launch_rope<64, float, false, false>(p, true, vec, grid, st);
+        if (d == 128) launch_rope<128, float, false, false>(p, true, vec, info->num_sms, st);
+        else launch_rope<64, float, false, false>(p, true, vec, info->num_sms, st);
     } else {
-        if (d == 128) launch_rope<128, __nv_bfloat16, false, false>(p, true, vec, grid, st);
-        else launch_rope<64, __nv_bfloat16, false, false>(p, true, vec, grid, st);
+        if (d == 128) launch_rope<128, __nv_bfloat16, false, false>(p, true, vec, info->num_sms, st);
+        else launch_rope<64, __nv_bfloat16, false, false>(p, true, vec, info->num_sms, st);
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(FA_ERR_CUDA, "rope launch: %s", cudaGetErrorString(e));

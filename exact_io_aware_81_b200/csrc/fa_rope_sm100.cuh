@@ -11,11 +11,13 @@
 // turns, reduced to [-1/2, 1/2] exactly there, and only then rounded to 32 bits for
 // sincospif.  The rotation runs in 32 bits and is rounded once, to the output's type.
 //
-// Bound: HBM (every element is read once and written once, about 3 flops per element).  One
-// warp takes one token (or, with few tokens, a share of one token's rows): a lane owns the
-// same two 16-byte chunks of every row, so its sines and cosines are computed once per token
-// and stay in registers over all heads of q and k.  kRowUnroll rows per lane are loaded before
-// the first is used, to keep enough bytes in flight.
+// Bound: HBM (every element is read once and written once, about 3 flops per element).  A CTA
+// takes `tokens` tokens (few tokens: a share of one token's rows): its threads compute the
+// tokens' sines and cosines once, into shared memory, then go over the rows, 2 x 16 bytes per
+// thread, the angles read back as needed, so few registers are held and many warps keep loads
+// in flight.  (16384 tokens of 32 + 8 heads, d = 128, bf16: 55.7 us = 6.0 TB/s, 0.92 of a plain
+// copy; a warp per token with the angles in registers, 105 of them, ran
+// at 4.8 TB/s.)
 //
 // PAGES: k and v rows go to row p % page_size of page block_table[b][p / page_size], p the
 // token's position in its sequence's cache, as bf16 or (FP8) as E4M3 bytes of value / scale.
@@ -38,7 +40,8 @@ struct RopeParams {
     const int *axes;         // (F), or null: all axis 0
     int T, Hq, Hkv, F, A;
     int interleaved, inverse;
-    int split;               // warps per token
+    int split;               // shares of a CTA's rows, over as many CTAs (the any-F kernel: warps per token)
+    int tokens;              // tokens of a CTA
     // pages only
     void *kpages, *vpages;   // (num_pages, Hkv, page_size, d)
     const float *k_scale, *v_scale;
@@ -50,8 +53,10 @@ struct RopeParams {
 
 namespace rope {
 
-constexpr int kWarps = 8;       // warps per CTA
-constexpr int kRowUnroll = 4;   // rows in flight per lane
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 4;      // most tokens of a CTA
+constexpr long long kPadding = -2;  // place of a token behind the last sequence
 
 template <typename T>
 struct Vec {
@@ -84,15 +89,17 @@ __device__ __forceinline__ uint4 pack(const float (&f)[4], float)
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
-// Eight values / scale as E4M3 bytes, round to nearest even, saturated to +-448 (a NaN stays
-// one).  The division is the correctly rounded one, so the byte depends on the value alone.
-__device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float scale)
+// Eight values times 1 / scale as E4M3 bytes, round to nearest even, saturated to +-448 (a NaN
+// stays one).  The reciprocal, rounded once per row to 32 bits, instead of a division per value:
+// the quotient is then off by at most 1.5 steps of 32 bits before it is rounded to 4 bits, and 16
+// divisions per thread and row made the append of a prompt batch 15% slower.
+__device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float inv_scale)
 {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)),
-                                        __NV_SATFINITE, __NV_E4M3);
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv_scale, f[2 * i + 1] * inv_scale), __NV_SATFINITE,
+                                        __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -161,141 +168,162 @@ __device__ __forceinline__ bool page_row_of(const RopeParams &p, int t, long lon
 // bytes) instead of k_out.  ROT: rotate q and k (else k and v are only stored).  VEC: every
 // 16-byte chunk is rotated by whole chunks of pairs (F a multiple of the chunk's elements,
 // or of half of them when interleaved) or not at all; otherwise pairs are taken one by one.
-template <int D, typename T, bool PAGES, bool FP8, bool ROT, bool VEC>
-__global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_kernel(const RopeParams p)
+template <int D, typename T, bool PAGES, bool FP8, bool ROT>
+__global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParams p)
 {
     using namespace rope;
     constexpr int V = Vec<T>::N;           // elements per 16-byte chunk
     constexpr int CH = D / V;              // chunks per row
-    constexpr int LANES = CH / 2;          // lanes per row, two chunks each
-    constexpr int ROWS = 32 / LANES;       // rows a warp takes at a time
-    static_assert(LANES <= 32 && 32 % LANES == 0, "row layout");
+    constexpr int LANES = CH / 2;          // threads per row, two chunks each
+    constexpr int STEP = kThreads / LANES; // rows the CTA takes at a time
+    constexpr int QV = V / 4;              // float4s of V angles
+    constexpr int kUnroll = FP8 ? 1 : 3;   // rows in flight per thread (registers against warps)
     static_assert(!FP8 || V == 8, "FP8 pages are written from bf16 rows");
+    // cos and sin of frequency lc * V + 4 q + e of token t at [t][q][lc].e: the threads of a row
+    // read consecutive 16-byte words
+    __shared__ float4 cos_t[ROT ? kTokens : 1][QV][LANES], sin_t[ROT ? kTokens : 1][QV][LANES];
+    __shared__ long long page_rows[kTokens];
 
-    const int lane = threadIdx.x & 31;
-    const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int n_warps = gridDim.x * kWarps;
-    const int lr = lane / LANES, lc = lane % LANES;
+    const int tid = threadIdx.x;
+    const int part = blockIdx.x % p.split;
+    const int t0 = (int)(blockIdx.x / p.split) * p.tokens;
+    const int nt = min(p.tokens, p.T - t0);
+    const int n_rows = p.Hq + p.Hkv + (PAGES ? p.Hkv : 0);
+    const int lc = tid % LANES;
 
-    // This lane's two chunks, and the frequency of each of its pairs (the same for every token).
+    // Chunks of this thread in every row, and whether each is rotated.
     const int FC = p.F / V;  // half-split: chunks of x elements
-    int ca, cb;
+    int ca = 2 * lc, cb = 2 * lc + 1;
     bool rot_a = false, rot_b = false;
-    if (ROT && VEC && !p.interleaved) {
+    if (ROT && !p.interleaved) {
+        // chunk c < FC pairs with c + FC; from 2 FC on elements are copied
         if (lc < FC) {
             ca = lc;
             cb = lc + FC;
             rot_a = rot_b = true;
-        } else {
-            ca = 2 * lc;  // 2 FC + 2 (lc - FC)
-            cb = ca + 1;
         }
-    } else {
-        ca = 2 * lc;
-        cb = ca + 1;
-        rot_a = ROT && VEC && (ca + 1) * V <= 2 * p.F;
-        rot_b = ROT && VEC && (cb + 1) * V <= 2 * p.F;
+    } else if (ROT) {
+        rot_a = (ca + 1) * V <= 2 * p.F;
+        rot_b = (cb + 1) * V <= 2 * p.F;
     }
-    const int f0 = lc * V;  // first of the V frequencies of the two chunks
-    const int n_rows = p.Hq + p.Hkv + (PAGES ? p.Hkv : 0);
 
-    for (long long item = warp; item < (long long)p.T * p.split; item += n_warps) {
-        const int t = (int)(item / p.split);
-        const int part = (int)(item - (long long)t * p.split);
-
-        long long page_row = -1;
-        if (PAGES && !page_row_of(p, t, page_row)) continue;  // behind the last sequence
-
-        float cs[V], sn[V];
-        if (ROT && VEC) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const bool used = p.interleaved ? (i < V / 2 ? rot_a : rot_b) : rot_a;
-                cs[i] = 1.f;
-                sn[i] = 0.f;
-                if (used) {
-                    const int f = f0 + i;
-                    angle(p.positions[(long long)axis_of(p, f) * p.T + t], p.inv_freq[f], p.inverse, cs[i], sn[i]);
-                }
-            }
+    // Where the tokens' k and v go: a warp per token.
+    if (PAGES) {
+        for (int i = tid >> 5; i < nt; i += kThreads / 32) {
+            long long row;
+            const bool real = page_row_of(p, t0 + i, row);
+            if ((tid & 31) == 0) page_rows[i] = real ? row : kPadding;
         }
+    }
+    if (ROT) {
+        float *ct = reinterpret_cast<float *>(cos_t), *st = reinterpret_cast<float *>(sin_t);
+        for (int i = tid; i < nt * p.F; i += kThreads) {
+            const int t = i / p.F, f = i - t * p.F;
+            float c, sn;
+            angle(p.positions[(long long)axis_of(p, f) * p.T + t0 + t], p.inv_freq[f], p.inverse, c, sn);
+            const int l = f / V, e = f % V;
+            const int at = ((t * QV + e / 4) * LANES + l) * 4 + e % 4;
+            ct[at] = c;
+            st[at] = sn;
+        }
+    }
+    __syncthreads();
 
-        // rows of this warp: ROWS at a time, kRowUnroll times
-        for (int r0 = part * ROWS; r0 < n_rows; r0 += p.split * ROWS * kRowUnroll) {
-            uint4 xa[kRowUnroll], xb[kRowUnroll];
-            const T *src[kRowUnroll];
+    // Rows part * STEP + tid / LANES, ... of the CTA's tokens, token by token.
+    int tok = 0, row = part * STEP + tid / LANES;
+    const int hop = p.split * STEP;
+    auto settle = [&]() {
+        while (row >= n_rows && tok < nt) {
+            row -= n_rows;
+            ++tok;
+        }
+    };
+    settle();
+    while (tok < nt) {
+        uint4 xa[kUnroll], xb[kUnroll];
+        int toks[kUnroll], rows[kUnroll];
 #pragma unroll
-            for (int u = 0; u < kRowUnroll; ++u) {
-                const int r = r0 + u * p.split * ROWS + lr;
-                src[u] = nullptr;
-                if (r < p.Hq) src[u] = static_cast<const T *>(p.q) + t * p.q_s + (long long)r * D;
-                else if (r < p.Hq + p.Hkv) src[u] = static_cast<const T *>(p.k) + t * p.k_s + (long long)(r - p.Hq) * D;
-                else if (r < n_rows) src[u] = static_cast<const T *>(p.v) + t * p.v_s + (long long)(r - p.Hq - p.Hkv) * D;
-                if (src[u]) {
-                    xa[u] = *reinterpret_cast<const uint4 *>(src[u] + ca * V);
-                    xb[u] = *reinterpret_cast<const uint4 *>(src[u] + cb * V);
-                }
+        for (int u = 0; u < kUnroll; ++u) {
+            toks[u] = tok;
+            rows[u] = row;
+            if (tok < nt) {
+                const long long t = t0 + tok;
+                const T *src = row < p.Hq           ? static_cast<const T *>(p.q) + t * p.q_s + (long long)row * D
+                               : row < p.Hq + p.Hkv ? static_cast<const T *>(p.k) + t * p.k_s + (long long)(row - p.Hq) * D
+                                                    : static_cast<const T *>(p.v) + t * p.v_s +
+                                                          (long long)(row - p.Hq - p.Hkv) * D;
+                xa[u] = *reinterpret_cast<const uint4 *>(src + ca * V);
+                xb[u] = *reinterpret_cast<const uint4 *>(src + cb * V);
             }
+            row += hop;
+            settle();
+        }
 #pragma unroll
-            for (int u = 0; u < kRowUnroll; ++u) {
-                const int r = r0 + u * p.split * ROWS + lr;
-                const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv;
-                const bool turn = ROT && VEC && (is_q || is_k);
-                float a[V], b[V];
-                if (turn || FP8) {
-                    unpack(xa[u], a, T());
-                    unpack(xb[u], b, T());
+        for (int u = 0; u < kUnroll; ++u) {
+            if (toks[u] >= nt) continue;
+            const long long t = t0 + toks[u];
+            const int r = rows[u];
+            const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv;
+            const long long place = PAGES ? page_rows[toks[u]] : 0;
+            if (PAGES && place == kPadding) continue;  // behind the last sequence: nothing is written
+            float a[V], b[V];
+            const bool turn = ROT && (is_q || is_k) && (rot_a || rot_b);
+            if (turn || FP8) {
+                unpack(xa[u], a, T());
+                unpack(xb[u], b, T());
+            }
+            if (turn) {
+                float cs[V], sn[V];
+#pragma unroll
+                for (int q = 0; q < QV; ++q) {
+                    const float4 c = cos_t[toks[u]][q][lc], d = sin_t[toks[u]][q][lc];
+                    cs[4 * q] = c.x, cs[4 * q + 1] = c.y, cs[4 * q + 2] = c.z, cs[4 * q + 3] = c.w;
+                    sn[4 * q] = d.x, sn[4 * q + 1] = d.y, sn[4 * q + 2] = d.z, sn[4 * q + 3] = d.w;
                 }
-                if (turn) {
-                    if (!p.interleaved) {
+                if (!p.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float x = a[i], y = b[i];
+                        a[i] = x * cs[i] - y * sn[i];
+                        b[i] = x * sn[i] + y * cs[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V / 2; ++i) {
+                        const float x = a[2 * i], y = a[2 * i + 1];
                         if (rot_a) {
-#pragma unroll
-                            for (int i = 0; i < V; ++i) {
-                                const float x = a[i], y = b[i];
-                                a[i] = x * cs[i] - y * sn[i];
-                                b[i] = x * sn[i] + y * cs[i];
-                            }
+                            a[2 * i] = x * cs[i] - y * sn[i];
+                            a[2 * i + 1] = x * sn[i] + y * cs[i];
                         }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V / 2; ++i) {
-                            if (rot_a) {
-                                const float x = a[2 * i], y = a[2 * i + 1];
-                                a[2 * i] = x * cs[i] - y * sn[i];
-                                a[2 * i + 1] = x * sn[i] + y * cs[i];
-                            }
-                            if (rot_b) {
-                                const float x = b[2 * i], y = b[2 * i + 1];
-                                b[2 * i] = x * cs[V / 2 + i] - y * sn[V / 2 + i];
-                                b[2 * i + 1] = x * sn[V / 2 + i] + y * cs[V / 2 + i];
-                            }
+                        const float z = b[2 * i], w = b[2 * i + 1];
+                        if (rot_b) {
+                            b[2 * i] = z * cs[V / 2 + i] - w * sn[V / 2 + i];
+                            b[2 * i + 1] = z * sn[V / 2 + i] + w * cs[V / 2 + i];
                         }
                     }
-                    if (rot_a) xa[u] = pack(a, T());
-                    if (rot_b) xb[u] = pack(b, T());
                 }
-                if (is_q || (is_k && !PAGES)) {
-                    T *dst = is_q ? static_cast<T *>(p.q_out) + t * p.qo_s + (long long)r * D
-                                  : static_cast<T *>(p.k_out) + t * p.ko_s + (long long)(r - p.Hq) * D;
+                if (rot_a) xa[u] = pack(a, T());
+                if (rot_b) xb[u] = pack(b, T());
+            }
+            if (is_q || (is_k && !PAGES)) {
+                T *dst = is_q ? static_cast<T *>(p.q_out) + t * p.qo_s + (long long)r * D
+                              : static_cast<T *>(p.k_out) + t * p.ko_s + (long long)(r - p.Hq) * D;
+                *reinterpret_cast<uint4 *>(dst + ca * V) = xa[u];
+                *reinterpret_cast<uint4 *>(dst + cb * V) = xb[u];
+            } else if (PAGES && place >= 0) {
+                const int h = is_k ? r - p.Hq : r - p.Hq - p.Hkv;
+                const long long at = (place + (long long)h * p.page_size) * D;
+                void *pool = is_k ? p.kpages : p.vpages;
+                if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
+                if constexpr (FP8) {
+                    const float inv_scale = __frcp_rn(is_k ? p.k_scale[h] : p.v_scale[h]);
+                    uint8_t *dst = static_cast<uint8_t *>(pool) + at;
+                    *reinterpret_cast<uint2 *>(dst + ca * V) = pack_e4m3(a, inv_scale);
+                    *reinterpret_cast<uint2 *>(dst + cb * V) = pack_e4m3(b, inv_scale);
+                } else {
+                    T *dst = static_cast<T *>(pool) + at;
                     *reinterpret_cast<uint4 *>(dst + ca * V) = xa[u];
                     *reinterpret_cast<uint4 *>(dst + cb * V) = xb[u];
-                } else if (PAGES && r < n_rows && page_row >= 0) {
-                    const int h = is_k ? r - p.Hq : r - p.Hq - p.Hkv;
-                    const long long at = (page_row + (long long)h * p.page_size) * D;
-                    void *pool = is_k ? p.kpages : p.vpages;
-                    if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
-                    if (FP8) {
-                        const float scale = is_k ? p.k_scale[h] : p.v_scale[h];
-                        uint8_t *dst = static_cast<uint8_t *>(pool) + at;
-                        if constexpr (V == 8) {
-                            *reinterpret_cast<uint2 *>(dst + ca * V) = pack_e4m3(a, scale);
-                            *reinterpret_cast<uint2 *>(dst + cb * V) = pack_e4m3(b, scale);
-                        }
-                    } else {
-                        T *dst = static_cast<T *>(pool) + at;
-                        *reinterpret_cast<uint4 *>(dst + ca * V) = xa[u];
-                        *reinterpret_cast<uint4 *>(dst + cb * V) = xb[u];
-                    }
                 }
             }
         }
@@ -352,10 +380,10 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
                     if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
                     void *pool = is_k ? p.kpages : p.vpages;
                     if (FP8) {
-                        const float scale = is_k ? p.k_scale[h] : p.v_scale[h];
+                        const float inv_scale = __frcp_rn(is_k ? p.k_scale[h] : p.v_scale[h]);
                         uint8_t *dst = static_cast<uint8_t *>(pool) + at;
-                        dst[i0] = __nv_cvt_float_to_fp8(__fdiv_rn(fx, scale), __NV_SATFINITE, __NV_E4M3);
-                        dst[i1] = __nv_cvt_float_to_fp8(__fdiv_rn(fy, scale), __NV_SATFINITE, __NV_E4M3);
+                        dst[i0] = __nv_cvt_float_to_fp8(fx * inv_scale, __NV_SATFINITE, __NV_E4M3);
+                        dst[i1] = __nv_cvt_float_to_fp8(fy * inv_scale, __NV_SATFINITE, __NV_E4M3);
                     } else {
                         static_cast<T *>(pool)[at + i0] = x;
                         static_cast<T *>(pool)[at + i1] = y;

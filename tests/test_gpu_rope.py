@@ -203,7 +203,7 @@ def test_cache_append(new, ctx, Hkv, d, ps, fp8):
     rows = serving.token_rows(table, cu, sl, ps, T)
     for got, pool, x, sc in ((kp, pools[0], k, scales[0]), (vp, pools[1], v, scales[1])):
         want = pool.clone()
-        src = serving.e4m3_bytes(x.float() / sc[:, None]) if fp8 else x
+        src = serving.e4m3_bytes(x.float() * (1 / sc)[:, None]) if fp8 else x
         for t, at in enumerate(rows):
             if at is not None:
                 want[at[0], :, at[1]] = src[t]
@@ -249,13 +249,13 @@ def test_rope_append(new, ctx, fp8, F, inter):
     want_v, touched = pools[1].clone(), torch.zeros(pools[0].shape[:3], dtype=torch.bool)
     for t in range(n):
         pg, r = rows[t]
-        want_v[pg, :, r] = serving.e4m3_bytes(v[t].float() / scales[1][:, None]) if fp8 else v[t]
+        want_v[pg, :, r] = serving.e4m3_bytes(v[t].float() * (1 / scales[1])[:, None]) if fp8 else v[t]
         touched[pg, :, r] = True
         if fp8:
             got = kc[pg, :, r].view(torch.float8_e4m3fn).double()
             ref, dd = rk[t] / scales[0].double()[:, None], dk[t] / scales[0].double()[:, None]
             ref = ref.clamp(-448, 448)
-            # half a step of E4M3 (2^-4 relative, 2^-10 among subnormals), the division's 2^-24
+            # half a step of E4M3 (2^-4 relative, 2^-10 among subnormals), the scaling's two roundings
             tol = 2.0 ** -4 * (ref.abs() + dd) + 2.0 ** -10 + dd + 2.0 ** -23 * ref.abs()
             assert ((got - ref).abs() <= tol).all()
         else:
