@@ -491,24 +491,38 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
 # --------------- packed sequences, rotary positions, cache filling, page management
 #
 # These calls are short (a few microseconds on the device), so their checks are the plain
-# ones below: one pass over each tensor's attributes, and the device is switched only when
-# the tensors are not on the current one.
+# ones below: one pass over each tensor's attributes, devices compared by index, and the device
+# switched only when the tensors are not on the current one.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without an object
 
 
-def _tensor(t, name, dtype, ndim, dev=None):
-    """A contiguous CUDA tensor of this type and rank (on `dev`)."""
+def _device_of(t, name) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != dtype or t.dim() != ndim or not t.is_contiguous():
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _other_device(t, name, dev):
+    return ValueError(f"all tensors must be on cuda:{dev}; found {name} on {t.device}")
+
+
+def _tensor(t, name, dtype, ndim, dev):
+    """The pointer of a contiguous CUDA tensor of this type and rank on device number `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or not t.is_contiguous():
         _require(t, name, dtype, ndim)
-    if dev is not None and t.device != dev:
-        raise ValueError(f"all tensors must be on {dev}; found {name} on {t.device}")
+    if t.get_device() != dev:
+        raise _other_device(t, name, dev)
     return t.data_ptr()
 
 
-def _rows(t, name, dtypes, dev=None):
+def _rows(t, name, dtypes, dev):
     """A (T, H, d) CUDA tensor whose heads are contiguous; tokens may be strided.  Returns
-    (pointer, token stride in elements)."""
+    (pointer, token stride in elements, T, H, d)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -519,20 +533,28 @@ def _rows(t, name, dtypes, dev=None):
         raise ValueError(f"{name} must have 3 dimensions (tokens, heads, d), got {t.dim()}")
     T, H, d = t.shape
     st, sh, sd = t.stride()
-    if (d > 1 and sd != 1) or (H > 1 and sh != d) or (T > 1 and st < H * d):
+    if T <= 1:
+        st = H * d
+    if (sd != 1 and d > 1) or (sh != d and H > 1) or st < H * d:
         raise ValueError(f"{name} must have contiguous heads (strides (*, d, 1)), got {t.stride()}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"all tensors must be on {dev}; found {name} on {t.device}")
-    return t.data_ptr(), (st if T > 1 else H * d)
+    if t.get_device() != dev:
+        raise _other_device(t, name, dev)
+    return t.data_ptr(), st, T, H, d
 
 
 def _launch(fn, dev, stream, *args):
-    """Call the library with the tensors' device current, on `stream` or its current stream."""
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _stream_handle(stream, dev))
+    """Call the library with device number `dev` current, on `stream` or its current stream."""
+    if stream is not None:
+        handle = int(stream.cuda_stream)
+    elif _raw_stream is not None:
+        handle = _raw_stream(dev)
+    else:
+        handle = int(torch.cuda.current_stream(dev).cuda_stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _stream_handle(stream, dev))
+            rc = fn(*args, handle)
     if rc != FA_OK:
         _check(rc)
 
@@ -543,24 +565,24 @@ def _scratch(workspace, need, dev):
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    elif workspace.device != dev:
-        raise ValueError(f"all tensors must be on {dev}; found workspace on {workspace.device}")
+    elif workspace.get_device() != dev:
+        raise _other_device(workspace, "workspace", dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _rotation(positions, inv_freq, axes, T, d, dev):
+def _rotation(positions, inv_freq, axes, T, dev):
     """Pointers and sizes of the rotation's tables: positions (T,) or (A, T), inv_freq (F,)."""
-    if isinstance(positions, torch.Tensor) and positions.dim() == 1:
-        positions = positions.unsqueeze(0)
-    pp = _tensor(positions, "positions", torch.int32, 2, dev)
+    one = isinstance(positions, torch.Tensor) and positions.dim() == 1
+    pp = _tensor(positions, "positions", torch.int32, 1 if one else 2, dev)
     pf = _tensor(inv_freq, "inv_freq", torch.float32, 1, dev)
-    A, F = positions.shape[0], inv_freq.shape[0]
-    if positions.shape[1] != T:
+    A, n = (1, positions.numel()) if one else positions.shape
+    F = inv_freq.numel()
+    if n != T:
         raise ValueError(f"positions must cover {T} tokens, got {tuple(positions.shape)}")
     pa = None
     if axes is not None:
         pa = _tensor(axes, "axes", torch.int32, 1, dev)
-        if axes.shape[0] != F:
+        if axes.numel() != F:
             raise ValueError("axes and inv_freq must have the same length")
     elif A != 1:
         raise ValueError("several position axes need `axes`, the axis of each frequency")
@@ -600,16 +622,15 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     the former).  Returns (o (Tq,Hq,d), lse fp32 (Hq,Tq)); causal is bottom-right aligned in each
     sequence, a row that sees no key gives o = 0 and lse = -inf.  ``workspace`` is a uint8 CUDA
     tensor of varlen_workspace_size(B, Tq, Hq, Hkv) bytes; one is allocated if omitted."""
-    dev = q.device
-    pq, sq = _rows(q, "q", _BF16, dev)
-    pk, sk = _rows(k, "k", _BF16, dev)
-    pv, sv = _rows(v, "v", _BF16, dev)
+    dev = _device_of(q, "q")
+    pq, sq, Tq, Hq, d = _rows(q, "q", _BF16, dev)
+    pk, sk, Tk, Hkv, dk = _rows(k, "k", _BF16, dev)
+    pv, sv, Tv, Hv, dv = _rows(v, "v", _BF16, dev)
     pcq = _tensor(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
     pck = pcq if cu_seqlens_k is None else _tensor(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1, dev)
-    Tq, Hq, d = q.shape
-    Tk, Hkv, dk = k.shape
-    B = cu_seqlens_q.shape[0] - 1
-    if dk != d or v.shape != k.shape or B < 1 or (cu_seqlens_k is not None and cu_seqlens_k.shape[0] != B + 1):
+    B = cu_seqlens_q.numel() - 1
+    if (dk != d or (Tv, Hv, dv) != (Tk, Hkv, dk) or B < 1
+            or (cu_seqlens_k is not None and cu_seqlens_k.numel() != B + 1)):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)} and the cu_seqlens")
     po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse)
     if scale is None:
@@ -631,13 +652,12 @@ def fwd_varlen_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
     cu_seqlens_q int32 (B+1,); sequence b attends the first seqlens[b] tokens of its pages (pools
     (num_pages,Hkv,page_size,d) bf16, block_table int32 (B,max_pages)), of which its rows are the
     last: chunked prefill, or a prompt that continues a shared prefix."""
-    dev = q.device
-    pq, sq = _rows(q, "q", _BF16, dev)
+    dev = _device_of(q, "q")
+    pq, sq, Tq, Hq, d = _rows(q, "q", _BF16, dev)
     pkp, pvp = _tensor(kpages, "kpages", torch.bfloat16, 4, dev), _tensor(vpages, "vpages", torch.bfloat16, 4, dev)
     pbt = _tensor(block_table, "block_table", torch.int32, 2, dev)
     pcq = _tensor(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1, dev)
     psl = _tensor(seqlens, "seqlens", torch.int32, 1, dev)
-    Tq, Hq, d = q.shape
     num_pages, Hkv, page_size, dk = kpages.shape
     B, max_pages = block_table.shape
     if dk != d or vpages.shape != kpages.shape or seqlens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
@@ -664,58 +684,62 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
     if q is None and k is None:
         raise ValueError("q and k cannot both be None")
     first = q if q is not None else k
-    if not isinstance(first, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dev, dtype = first.device, first.dtype
-    ptrs, strides, heads, outs = [], [], [], []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            ptrs.append((None, None))
-            strides.append((0, 0))
-            heads.append(0)
-            outs.append(None)
-            continue
-        p, s = _rows(x, name, _ROPE_TYPES, dev)
-        if x.dtype != dtype or x.shape[0] != first.shape[0] or x.shape[2] != first.shape[2]:
-            raise ValueError("q and k must have the same type, tokens and head dim")
-        if out is None:
-            out = torch.empty(x.shape, dtype=dtype, device=dev)
-        po, so = _rows(out, name + "_out", (dtype,), dev)
-        if out.shape != x.shape:
-            raise ValueError(f"{name}_out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        ptrs.append((p, po))
-        strides.append((s, so))
-        heads.append(x.shape[1])
-        outs.append(out)
-    T, d = first.shape[0], first.shape[2]
-    pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, d, dev)
-    if T == 0:
-        return outs[0], outs[1]
-    _launch(load().fa_rope, dev, stream, ptrs[0][0], ptrs[1][0], ptrs[0][1], ptrs[1][1], pp, pf, pa, T, heads[0],
-            heads[1], d, F, A, strides[0][0], strides[1][0], strides[0][1], strides[1][1],
-            FA_F32 if dtype == torch.float32 else FA_BF16, int(bool(interleaved)), int(bool(inverse)))
-    return outs[0], outs[1]
+    dev = _device_of(first, "q" if q is not None else "k")
+    types = (first.dtype,) if first.dtype in _ROPE_TYPES else _ROPE_TYPES
+    pq, sq, pqo, sqo, Tq, Hq, dq = _turned(q, q_out, "q", types, dev) if q is not None else _NOTHING
+    pk, sk, pko, sko, Tk, Hk, dk = _turned(k, k_out, "k", types, dev) if k is not None else _NOTHING
+    if q is not None and k is not None and (Tq, dq) != (Tk, dk):
+        raise ValueError("q and k must have the same tokens and head dim")
+    T, d = (Tq, dq) if q is not None else (Tk, dk)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        pqo, sqo = q_out.data_ptr(), Hq * dq
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        pko, sko = k_out.data_ptr(), Hk * dk
+    if q is None:
+        q_out = None
+    if k is None:
+        k_out = None
+    pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, dev)
+    if T > 0:
+        _launch(load().fa_rope, dev, stream, pq, pk, pqo, pko, pp, pf, pa, T, Hq, Hk, d, F, A, sq, sk, sqo, sko,
+                FA_F32 if first.dtype is torch.float32 else FA_BF16, 1 if interleaved else 0, 1 if inverse else 0)
+    return q_out, k_out
+
+
+_NOTHING = (None, 0, None, 0, 0, 0, 0)
+
+
+def _turned(x, out, name, types, dev):
+    """Pointers, strides and sizes of one of rope's tensors and its output (if given)."""
+    p, st, T, H, d = _rows(x, name, types, dev)
+    if out is None:
+        return p, st, None, 0, T, H, d
+    po, so, To, Ho, do = _rows(out, name + "_out", types, dev)
+    if (To, Ho, do) != (T, H, d):
+        raise ValueError(f"{name}_out must have shape {(T, H, d)}, got {tuple(out.shape)}")
+    return p, st, po, so, T, H, d
 
 
 def _destination(k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev):
     """The checks fa_cache_append and fa_rope_append share: (k, v) rows and the pages' arguments."""
-    pk, sk = _rows(k, "k", _BF16, dev)
-    pv, sv = _rows(v, "v", _BF16, dev)
-    T, Hkv, d = k.shape
+    pk, sk, T, Hkv, d = _rows(k, "k", _BF16, dev)
+    pv, sv, Tv, Hv, dv = _rows(v, "v", _BF16, dev)
     fp8 = k_scale is not None or v_scale is not None
     pool = torch.uint8 if fp8 else torch.bfloat16
     pkp, pvp = _tensor(kpages, "kpages", pool, 4, dev), _tensor(vpages, "vpages", pool, 4, dev)
     pks = pvs = None
     if fp8:
         pks, pvs = _tensor(k_scale, "k_scale", torch.float32, 1, dev), _tensor(v_scale, "v_scale", torch.float32, 1, dev)
-        if k_scale.shape[0] != Hkv or v_scale.shape[0] != Hkv:
+        if k_scale.numel() != Hkv or v_scale.numel() != Hkv:
             raise ValueError("k_scale and v_scale must have Hkv entries")
     pbt = _tensor(block_table, "block_table", torch.int32, 2, dev)
     pcu, psl = _tensor(cu_seqlens, "cu_seqlens", torch.int32, 1, dev), _tensor(seqlens, "seqlens", torch.int32, 1, dev)
     num_pages, H, page_size, dk = kpages.shape
     B, max_pages = block_table.shape
-    if (v.shape != k.shape or (H, dk) != (Hkv, d) or vpages.shape != kpages.shape or seqlens.shape[0] != B
-            or cu_seqlens.shape[0] != B + 1):
+    if ((Tv, Hv, dv) != (T, Hkv, d) or (H, dk) != (Hkv, d) or vpages.shape != kpages.shape or seqlens.numel() != B
+            or cu_seqlens.numel() != B + 1):
         raise ValueError("shape mismatch between k, v, the pools, block_table, cu_seqlens and seqlens")
     return (pk, sk), (pv, sv), (pkp, pvp, pks, pvs, pbt, pcu, psl), (T, B, Hkv, num_pages, page_size, max_pages, d)
 
@@ -726,7 +750,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, kpages: torch.Tensor, vpages:
     """Put new tokens' k and v (T,Hkv,d), packed by cu_seqlens int32 (B+1,), into the pages
     (fa_cache_append): the last positions of sequences of length seqlens (which include them).
     Pools (num_pages,Hkv,page_size,d) bf16, or uint8 E4M3 with k_scale / v_scale fp32 (Hkv,)."""
-    dev = kpages.device
+    dev = _device_of(kpages, "kpages")
     (pk, sk), (pv, sv), ptrs, (T, B, Hkv, num_pages, page_size, max_pages, d) = _destination(
         k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev)
     if T == 0:
@@ -741,43 +765,39 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
                 v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
     """rope of q and k and cache_append of the rotated k and of v in one launch
     (fa_rope_append).  Returns q_out (None if q is None)."""
-    dev = kpages.device
+    dev = _device_of(kpages, "kpages")
     (pk, sk), (pv, sv), ptrs, (T, B, Hkv, num_pages, page_size, max_pages, d) = _destination(
         k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev)
     pq = po = None
     sq = so = Hq = 0
     if q is not None:
-        pq, sq = _rows(q, "q", _BF16, dev)
-        Hq = q.shape[1]
-        if q.shape[0] != T or q.shape[2] != d:
-            raise ValueError("q and k must have the same tokens and head dim")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        po, so = _rows(q_out, "q_out", _BF16, dev)
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out must have shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
-    pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, d, dev)
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        pq, sq, po, so, Tq, Hq, dq = _turned(q, q_out, "q", _BF16, dev)
+        if (Tq, dq) != (T, d):
+            raise ValueError("q and k must have the same tokens and head dim")
+    pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, dev)
     if T == 0:
         return q_out
     _launch(load().fa_rope_append, dev, stream, pq, pk, pv, po, pp, pf, pa, *ptrs, T, B, Hq, Hkv, num_pages,
-            page_size, max_pages, d, F, A, sq, sk, sv, so, int(bool(interleaved)))
+            page_size, max_pages, d, F, A, sq, sk, sv, so, 1 if interleaved else 0)
     return q_out
 
 
 def _page_state(block_table, seqlens, refcount):
-    dev = block_table.device if isinstance(block_table, torch.Tensor) else None
-    ptrs = (_tensor(block_table, "block_table", torch.int32, 2), _tensor(seqlens, "seqlens", torch.int32, 1, dev),
+    dev = _device_of(block_table, "block_table")
+    ptrs = (_tensor(block_table, "block_table", torch.int32, 2, dev), _tensor(seqlens, "seqlens", torch.int32, 1, dev),
             _tensor(refcount, "refcount", torch.int32, 1, dev))
     S, max_pages = block_table.shape
-    if seqlens.shape[0] != S:
+    if seqlens.numel() != S:
         raise ValueError("block_table and seqlens must have the same number of slots")
-    return dev, ptrs, (S, max_pages, refcount.shape[0])
+    return dev, ptrs, (S, max_pages, refcount.numel())
 
 
 def _list(t, name, n, dev):
     p = _tensor(t, name, torch.int32, 1, dev)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
     return p
 
 
@@ -818,7 +838,7 @@ def pages_fork(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch
     their pages (fa_pages_fork)."""
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     ps = _tensor(src, "src", torch.int32, 1, dev)
-    n = src.shape[0]
+    n = src.numel()
     pd = _list(dst, "dst", n, dev)
     pl = _list(lengths, "lengths", n, dev) if lengths is not None else None
     if n == 0:
@@ -832,7 +852,7 @@ def pages_free(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch
     behind them (fa_pages_free)."""
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     ps = _tensor(slots, "slots", torch.int32, 1, dev)
-    n = slots.shape[0]
+    n = slots.numel()
     pk = _list(keep, "keep", n, dev) if keep is not None else None
     if n == 0:
         return
@@ -854,12 +874,10 @@ def pages_compact(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
 def pages_copy(kpages: torch.Tensor, vpages: Optional[torch.Tensor], copies: torch.Tensor, stream=None):
     """Copy page copies[i,0] to page copies[i,1] in both pools (fa_pages_copy); -1 is skipped.
     Pools (num_pages,Hkv,page_size,d), bf16 or uint8."""
-    if not isinstance(kpages, torch.Tensor):
-        raise TypeError("kpages must be a torch.Tensor")
-    dev, dtype = kpages.device, kpages.dtype
+    dev, dtype = _device_of(kpages, "kpages"), kpages.dtype
     if dtype not in (torch.bfloat16, torch.uint8):
         raise ValueError(f"kpages must be bfloat16 or uint8, got {dtype}")
-    pk = _tensor(kpages, "kpages", dtype, 4)
+    pk = _tensor(kpages, "kpages", dtype, 4, dev)
     pv = None
     if vpages is not None:
         pv = _tensor(vpages, "vpages", dtype, 4, dev)
