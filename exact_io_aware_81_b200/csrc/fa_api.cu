@@ -1266,7 +1266,7 @@ int fa_pages_compact(int *block_table, int *seqlens, int *refcount, int *copies,
     if ((rc = check_workspace(workspace, workspace_bytes, compact_ws_bytes(num_pages))) != FA_OK) return rc;
     p.copies = copies;
     p.n_live = static_cast<int *>(workspace);
-    p.map = reinterpret_cast<int *>(static_cast<char *>(workspace) + 256);
+    p.rank = reinterpret_cast<int *>(static_cast<char *>(workspace) + 256);
     p.holes = reinterpret_cast<int *>(static_cast<char *>(workspace) + 256 + align256((size_t)num_pages * 4));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     fa::fa_pages_compact_kernel<<<1, fa::pages::kPlanThreads, 0, st>>>(p);
