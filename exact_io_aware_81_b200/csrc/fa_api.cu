@@ -115,6 +115,7 @@ struct MapKey {
 };
 constexpr int kMapCacheSize = 64;
 struct MapCache {
+    uint64_t hash[kMapCacheSize] = {};  // of the keys: one word to look at per entry
     MapKey key[kMapCacheSize];
     CUtensorMap map[kMapCacheSize];
     bool used[kMapCacheSize] = {};
@@ -122,6 +123,18 @@ struct MapCache {
 };
 MapCache g_maps;
 std::mutex g_maps_mu;
+
+uint64_t hash_key(const MapKey &k)
+{
+    static_assert(sizeof(MapKey) % 8 == 0, "hashed by words");
+    uint64_t w[sizeof(MapKey) / 8], h = 0;
+    memcpy(w, &k, sizeof k);
+    for (uint64_t x : w) {
+        h = (h ^ x) * 0x9E3779B97F4A7C15ull;
+        h ^= h >> 29;
+    }
+    return h;
+}
 
 int encode_map_cached(CUtensorMap *m, CUtensorMapDataType dtype, int rank, const void *base,
                       const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box)
@@ -136,10 +149,11 @@ int encode_map_cached(CUtensorMap *m, CUtensorMapDataType dtype, int rank, const
         k.box[i] = box[i];
         if (i + 1 < rank) k.strides[i] = strides[i];
     }
+    const uint64_t hash = hash_key(k);
     {
         std::lock_guard<std::mutex> lk(g_maps_mu);
         for (int i = 0; i < kMapCacheSize; ++i)
-            if (g_maps.used[i] && memcmp(&g_maps.key[i], &k, sizeof k) == 0) {
+            if (g_maps.hash[i] == hash && g_maps.used[i] && memcmp(&g_maps.key[i], &k, sizeof k) == 0) {
                 *m = g_maps.map[i];
                 return FA_OK;
             }
@@ -154,6 +168,7 @@ int encode_map_cached(CUtensorMap *m, CUtensorMapDataType dtype, int rank, const
     std::lock_guard<std::mutex> lk(g_maps_mu);
     const int slot = g_maps.next;
     g_maps.next = (slot + 1) % kMapCacheSize;
+    g_maps.hash[slot] = hash;
     g_maps.key[slot] = k;
     g_maps.map[slot] = *m;
     g_maps.used[slot] = true;
