@@ -714,7 +714,7 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     p.Hkv = Hkv;
     p.R = R;
     p.causal = causal ? 1 : 0;
-    p.window = window;
+    p.window = window < keys ? window : 0;  // a window of every key is plain causal
     p.pack = pack;
     p.tile_tokens = 128 / pack;
     p.slots = slots;
@@ -735,7 +735,7 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     m.Tk = (int)keys;
     m.rows = 2 * p.tile_tokens;
     m.causal = p.causal;
-    m.window = window;
+    m.window = p.window;
     // The variant for a few tokens against many keys -- many tiles without a partner, and units
     // that are few and long -- judged by the averages, the lengths being known on the device only.
     // Measured on B200 (32 + 8 heads, d = 128): 12 chunks of 1 to 512 tokens over contexts of up to
