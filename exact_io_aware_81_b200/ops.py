@@ -490,19 +490,25 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
 
 # --------------- packed sequences, rotary positions, cache filling, page management
 #
-# These calls are short (a few microseconds on the device), so their checks are the plain
-# ones below: one pass over each tensor's attributes, devices compared by index, and the device
-# switched only when the tensors are not on the current one.
+# These calls are short (a few microseconds on the device), so their checks come in two parts:
+# one expression that a right argument passes (devices compared by index), and, when it does not,
+# a function that finds out what is wrong.  The device is switched only when the tensors are not
+# on the current one.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without an object
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _device_of(t, name) -> int:
+    try:
+        dev = t.get_device()
+        if dev >= 0:
+            return dev
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    raise ValueError(f"{name} must be a CUDA tensor")
 
 
 def _other_device(t, name, dev):
@@ -511,18 +517,25 @@ def _other_device(t, name, dev):
 
 def _tensor(t, name, dtype, ndim, dev):
     """The pointer of a contiguous CUDA tensor of this type and rank on device number `dev`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or not t.is_contiguous():
-        _require(t, name, dtype, ndim)
-    if t.get_device() != dev:
-        raise _other_device(t, name, dev)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.dim() == ndim and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _require(t, name, dtype, ndim)
+    raise _other_device(t, name, dev)
 
 
 def _rows(t, name, dtypes, dev):
     """A (T, H, d) CUDA tensor whose heads are contiguous; tokens may be strided.  Returns
     (pointer, token stride in elements, T, H, d)."""
+    try:
+        T, H, d = t.shape
+        st, sh, sd = t.stride()
+        if sd == 1 and sh == d and st >= H * d and T > 1 and t.dtype in dtypes and t.get_device() == dev:
+            return t.data_ptr(), st, T, H, d
+    except (AttributeError, TypeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -531,14 +544,14 @@ def _rows(t, name, dtypes, dev):
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dimensions (tokens, heads, d), got {t.dim()}")
+    if t.get_device() != dev:
+        raise _other_device(t, name, dev)
     T, H, d = t.shape
     st, sh, sd = t.stride()
-    if T <= 1:
+    if T <= 1:  # the stride of a single token says nothing
         st = H * d
     if (sd != 1 and d > 1) or (sh != d and H > 1) or st < H * d:
         raise ValueError(f"{name} must have contiguous heads (strides (*, d, 1)), got {t.stride()}")
-    if t.get_device() != dev:
-        raise _other_device(t, name, dev)
     return t.data_ptr(), st, T, H, d
 
 
@@ -550,7 +563,7 @@ def _launch(fn, dev, stream, *args):
         handle = _raw_stream(dev)
     else:
         handle = int(torch.cuda.current_stream(dev).cuda_stream)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
