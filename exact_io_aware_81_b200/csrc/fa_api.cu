@@ -583,7 +583,7 @@ int launch_varlen(const fa::VarlenParams &p, int grid, DeviceInfo *info, cudaStr
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.plan ? 1 : 0;  // (without a plan kernel before it, it depends on what came before)
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess) return fail(FA_ERR_CUDA, "packed attention launch: %s", cudaGetErrorString(e));
     return FA_OK;
@@ -722,9 +722,8 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     p.wait_limit_ns = g_wait_limit_ns;
     p.plan_head = static_cast<int *>(workspace);
     int4 *plan = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + kVarlenHeadBytes);
-    p.plan = plan;
 
-    fa::VarlenPlanParams m;
+    fa::VarlenPlanParams &m = p.jobs;
     m.cu_q = cu_q;
     m.cu_k = c.cu_k;
     m.seqlens = c.paged ? c.seqlens : nullptr;
@@ -746,14 +745,18 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     m.twins = few ? 1 : 0;
     m.max_jobs = varlen_max_jobs(B, Tq, pack);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    fa::fa_varlen_plan_kernel<<<1, fa::varlen::kThreads, 0, st>>>(m);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(FA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));
     const long long bound = (long long)m.max_jobs * slots;
-    const int grid = bound < info->num_sms ? (int)bound : info->num_sms;
+    const bool wave = bound <= info->num_sms;  // no more units than CTAs: no order to plan
+    const int grid = wave ? (int)bound : info->num_sms;
+    if (!wave) {
+        p.plan = plan;
+        fa::fa_varlen_plan_kernel<<<1, fa::varlen::kThreads, 0, st>>>(m);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return fail(FA_ERR_CUDA, "plan launch: %s", cudaGetErrorString(e));
+    }
     const bool f32 = o_dtype == FA_F32;
-    rc = c.paged ? launch_varlen_variant<true>(p, d, f32, few, grid, info, st)
-                 : launch_varlen_variant<false>(p, d, f32, few, grid, info, st);
+    rc = c.paged ? launch_varlen_variant<true>(p, d, f32, few || wave, grid, info, st)
+                 : launch_varlen_variant<false>(p, d, f32, few || wave, grid, info, st);
     if (rc != FA_OK) return rc;
     return ok();
 }

@@ -15,7 +15,8 @@
 //   Order.  The lengths are known on the device only.  fa_varlen_plan_kernel lists the jobs (the
 //     tokens of two tiles of one sequence) by falling number of steps: a counting sort over
 //     kBins classes, whose order within a class is left open (it decides which CTA computes
-//     what, never a result).  The attention kernel's CTAs draw units (job x head slot) from a
+//     what, never a result; a call whose units fit one wave of CTAs goes without a plan, each
+//     CTA finding its own: 8 prompts of up to 64 tokens 12.4 -> 10.3 us).  The attention kernel's CTAs draw units (job x head slot) from a
 //     counter, longest first, so that they end together.  Only the producer warp draws; it hands
 //     each unit to the other roles through a ring of records in shared memory.
 //   Isolation.  A key tile that passes its sequence's end holds other rows (the next sequence's,
@@ -191,7 +192,8 @@ struct VarlenParams {
     CUtensorMap tm_o;  // (d, Hq, Tq) bf16 output, box (64, pack, 32 / pack): one warp's rows
     void *o;           // (Tq, Hq, d)
     float *lse;        // (Hq, Tq)
-    const int4 *plan;  // two per job: {q row of the sequence, Nq, k row, Nk}, {first token, sequence, -, -}
+    const int4 *plan;  // two per job: {q row of the sequence, Nq, k row, Nk}, {first token, sequence, -, -};
+                       // null: as many CTAs as units at most, each finds its own
     int *plan_head;    // [0] number of jobs, [1] units handed out so far
     int Tq, Hq, Hkv, R;
     int causal, window;
@@ -204,6 +206,7 @@ struct VarlenParams {
     const int *block_table;  // (B, max_pages)
     int B, page_size, max_pages, num_pages;
     int box_rows;            // rows per copy: a power of two <= 128 that divides page_size
+    VarlenPlanParams jobs;   // without a plan: what the jobs are made from
 };
 
 namespace varlen {
@@ -285,6 +288,37 @@ __device__ __forceinline__ void make_unit(const VarlenParams &p, const int4 &x, 
         w.n1 = w.n0;
         w.a1 = w.twin ? w.a0 + 1 : w.n0;
     }
+}
+
+// Job number `job` in order of the sequences, for a call without a plan; false behind the last.
+// Whole warp, 32 sequences a step.  Lengths out of range are reported by CTA 0.
+__device__ __forceinline__ bool find_job(const VarlenPlanParams &m, int job, int4 &x, int4 &y)
+{
+    const int lane = threadIdx.x & 31;
+    bool found = false, bad = false;
+    int base = 0;
+    for (int b0 = 0; b0 < m.B; b0 += 32) {
+        Seq s{0, 0, 0, 0};
+        if (b0 + lane < m.B) s = sequence(m, b0 + lane, bad);
+        const int n = (s.nq + m.rows - 1) / m.rows;
+        int upto = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, base + upto > job);
+        if (!found && hit) {
+            const int l = __ffs(hit) - 1;
+            x = make_int4(__shfl_sync(0xffffffffu, s.q0, l), __shfl_sync(0xffffffffu, s.nq, l),
+                          __shfl_sync(0xffffffffu, s.k0, l), __shfl_sync(0xffffffffu, s.nk, l));
+            y = make_int4((job - base - __shfl_sync(0xffffffffu, upto - n, l)) * m.rows, b0 + l, 0, 0);
+            found = true;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (__any_sync(0xffffffffu, bad) && blockIdx.x == 0 && lane == 0) raise_error(kErrCuSeqlens);
+    return found;
 }
 
 // Clear rows [first, 128) of a V tile (all slabs; the swizzle permutes within a row).  Whole warp.
@@ -426,8 +460,9 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
         // then, so neither the counter's nor the plan's latency holds up the K/V stream.  With few
         // (`late`), a number drawn early is a long unit dealt out blindly: unit i + 1 is then drawn
         // four key tiles before unit i's last, one step of its way per tile.
-        asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is complete
-        const int n_units = __ldcg(&p.plan_head[0]) * p.slots;
+        const bool alone = SHORT && p.plan == nullptr;  // one unit per CTA, found without a plan
+        if (!alone) asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is complete
+        const int n_units = alone ? 0 : __ldcg(&p.plan_head[0]) * p.slots;
         const bool late = SHORT && n_units < 4 * (int)gridDim.x;
         auto draw = [&]() { return leader ? (int)gridDim.x + atomicAdd(&p.plan_head[1], 1) : 0; };
         // A record's slot is reused four units later: Q(i) was issued, so unit i - 2 has released
@@ -499,12 +534,17 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
         int slot = 0, u = (int)blockIdx.x;
         int next_raw = late ? 0 : draw();
         uint32_t i = 0;
-        bool have = u < n_units;
-        if (have) {
-            const int job = u / p.slots;
-            slot = u - job * p.slots;
-            make_unit<WINDOW, SHORT>(p, __ldcg(&p.plan[2 * job]), __ldcg(&p.plan[2 * job + 1]), slot, w);
+        const int job0 = u / p.slots;
+        slot = u - job0 * p.slots;
+        int4 x0, y0;
+        bool have;
+        if (alone) {
+            have = find_job(p.jobs, job0, x0, y0);
+        } else if ((have = u < n_units)) {
+            x0 = __ldcg(&p.plan[2 * job0]);
+            y0 = __ldcg(&p.plan[2 * job0 + 1]);
         }
+        if (have) make_unit<WINDOW, SHORT>(p, x0, y0, slot, w);
         publish(0, have, w);
         for (int s = 0; ok && have && s < 2; ++s) {
             if (!wait_warp(q_slot(0, s), q_free_parity(0), sf)) ok = false;
@@ -516,8 +556,8 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
         for (; ok && have; ++i) {
             bool have_n = false;
             int4 px = make_int4(0, 0, 0, 0), py = px;  // the next unit's plan entry, in flight
-            int q_next = 0;                            // look-ahead Q tiles already issued
-            enum { kAsk, kLookUp, kTell, kTold } step = late ? kAsk : kLookUp;
+            int q_next = alone ? 2 : 0;                // look-ahead Q tiles already issued
+            enum { kAsk, kLookUp, kTell, kTold } step = alone ? kTell : late ? kAsk : kLookUp;
             auto ask = [&]() {
                 next_raw = draw();
                 step = kLookUp;

@@ -349,3 +349,25 @@ def test_refusals():
     assert status(lambda: ops.fwd_varlen(q, k, k, c, scale=0.0)) == ops.FA_ERR_INVALID
     small = torch.empty(16, device=DEV, dtype=torch.uint8)
     assert status(lambda: ops.fwd_varlen(q, k, k, c, workspace=small)) == ops.FA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 4, 128), (8, 2, 64), (3, 1, 128)])
+@pytest.mark.parametrize("B", [1, 31, 33, 70])
+def test_one_wave_of_units(B, Hq, Hkv, d):
+    """Few enough units for a CTA each: no plan is made, every CTA finds its own job -- among
+    sequences of no tokens, in every step of 32 sequences, and past the last job."""
+    g = torch.Generator().manual_seed(B)
+    n = [0] * B
+    for b in {0, B // 2, B - 1}:
+        n[b] = int(torch.randint(1, 60, (1,), generator=g))
+    n[B // 2] = 0 if B > 2 else n[B // 2]
+    if B > 32:
+        n[32] = 9
+    nk = [x + int(torch.randint(0, 700, (1,), generator=g)) for x in n]
+    q, k, v = make(n, nk, Hq, Hkv, d, 50 + B, pad_q=3, pad_k=2)
+    o, lse, status = run(q, k, v, cu(n), cu(nk), True)
+    assert status == ops.FA_OK
+    verify(o, lse, q, k, v, cu(n), cu(nk), True)
+    bad = cu(n)
+    bad[-1] = q.shape[0] + 1
+    assert run(q, k, v, bad, cu(nk), True)[2] == ops.FA_ERR_DEVICE_ARG
