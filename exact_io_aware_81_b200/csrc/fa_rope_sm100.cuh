@@ -16,11 +16,10 @@
 // tokens' sines and cosines once, into shared memory, then go over the rows, 2 x 16 bytes per
 // thread, the angles read back as needed, so few registers are held and many warps keep loads
 // in flight.  (16384 tokens of 32 + 8 heads, d = 128, bf16: 55.7 us = 6.0 TB/s, 0.92 of a plain
-// copy; a warp per token with the angles in registers, 105 of them, ran
-// at 4.8 TB/s.)
+// copy; a warp per token with the angles in registers, 105 of them, ran at 4.8 TB/s.)
 //
 // PAGES: k and v rows go to row p % page_size of page block_table[b][p / page_size], p the
-// token's position in its sequence's cache, as bf16 or (FP8) as E4M3 bytes of value / scale.
+// token's position in its sequence's cache, as bf16 or (FP8) as E4M3 bytes of the scaled value.
 #pragma once
 
 #include <cstdint>
@@ -165,9 +164,9 @@ __device__ __forceinline__ bool page_row_of(const RopeParams &p, int t, long lon
 }  // namespace rope
 
 // D: head dim.  T: element type of q, k, v.  PAGES: k and v go to the pages (FP8: as E4M3
-// bytes) instead of k_out.  ROT: rotate q and k (else k and v are only stored).  VEC: every
-// 16-byte chunk is rotated by whole chunks of pairs (F a multiple of the chunk's elements,
-// or of half of them when interleaved) or not at all; otherwise pairs are taken one by one.
+// bytes) instead of k_out.  ROT: rotate q and k (else k and v are only stored).  For frequency
+// counts with which every 16-byte chunk is rotated as a whole or not at all: F a multiple of a
+// chunk's elements, or of half of them when interleaved.
 template <int D, typename T, bool PAGES, bool FP8, bool ROT>
 __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParams p)
 {
