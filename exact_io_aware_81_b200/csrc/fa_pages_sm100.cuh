@@ -22,9 +22,9 @@
 // Bounds.  The bookkeeping touches kilobytes and is bound by latency: fork and free run one
 // CTA per slot; reserve and compact need sums over all slots or pages and run as one CTA of
 // 1024 threads (16 bytes of refcounts per thread and step), so each is one launch with no
-// grid-wide step.  The copy is bound by HBM: 16-byte loads, kCopyUnroll in flight per thread, both ways past
-// the caches' regular replacement (504 pages of 128 KB in two pools, 264 MB there and back:
-// 44 us = 6.0 TB/s; four loads without the hints 48).
+// grid-wide step.  The copy is bound by HBM: 16-byte loads, kCopyUnroll in flight per thread,
+// both ways past the caches' regular replacement (504 pages of 128 KB in two pools, 264 MB
+// there and back: 44 us = 6.0 TB/s; four loads without the hints 48).
 #pragma once
 
 #include <cstdint>
