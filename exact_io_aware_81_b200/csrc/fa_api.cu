@@ -1299,7 +1299,7 @@ int fa_pages_copy(void *kpages, void *vpages, const int *copies, int n, int num_
     if (!kpages || !copies) return fail(FA_ERR_INVALID, "null pointer argument");
     if (n < 0 || num_pages <= 0 || page_bytes <= 0)
         return fail(FA_ERR_INVALID, "sizes must be positive (n=%d num_pages=%d page_bytes=%lld)", n, num_pages, page_bytes);
-    if (page_bytes % 16 != 0 || page_bytes > (1LL << 46) / num_pages)
+    if (page_bytes % 16 != 0 || page_bytes > (1LL << 44) / num_pages)
         return fail(FA_ERR_UNSUPPORTED, "a page of %lld bytes is not a multiple of 16, or the pool is too large", page_bytes);
     if (!aligned16(kpages) || !aligned16(vpages))
         return fail(FA_ERR_UNSUPPORTED, "the page pools must be 16-byte aligned");

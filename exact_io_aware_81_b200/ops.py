@@ -572,11 +572,19 @@ def _launch(fn, dev, stream, *args):
         _check(rc)
 
 
-def _scratch(workspace, size, sizes, dev):
+def _scratch(workspace, size, sizes, dev, stream):
     """(pointer, bytes) of the caller's workspace, whose size the library checks, or of a new one of
-    size(*sizes) bytes (kept alive by the third)."""
+    size(*sizes) bytes (kept alive by the third).  A new one is memory of the stream that the call
+    runs on: it is given back when the call returns, and only work behind it may use it again."""
     if workspace is None:
-        workspace = torch.empty(max(size(*sizes), 16), dtype=torch.uint8, device=dev)
+        n = max(size(*sizes), 16)
+        if stream is None:
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream.cuda_stream), dev)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     elif workspace.get_device() != dev:
@@ -651,7 +659,7 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
         scale = 1.0 / math.sqrt(d)
     if Tq == 0:
         return out, lse
-    pw, nw, workspace = _scratch(workspace, varlen_workspace_size, (B, Tq, Hq, Hkv), dev)
+    pw, nw, workspace = _scratch(workspace, varlen_workspace_size, (B, Tq, Hq, Hkv), dev, stream)
     _launch(load().fa_fwd_varlen, dev, stream, pq, pk, pv, po, pl, pcq, pck, B, Tq, Tk, Hq, Hkv, d, sq, sk, sv,
             float(scale), int(bool(causal)), int(window), odt, pw, nw)
     return out, lse
@@ -681,7 +689,7 @@ def fwd_varlen_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
         scale = 1.0 / math.sqrt(d)
     if Tq == 0:
         return out, lse
-    pw, nw, workspace = _scratch(workspace, varlen_workspace_size, (B, Tq, Hq, Hkv), dev)
+    pw, nw, workspace = _scratch(workspace, varlen_workspace_size, (B, Tq, Hq, Hkv), dev, stream)
     _launch(load().fa_fwd_varlen_paged, dev, stream, pq, pkp, pvp, pbt, pcq, psl, po, pl, B, Tq, Hq, Hkv, num_pages,
             page_size, max_pages, d, sq, float(scale), int(bool(causal)), int(window), odt, pw, nw)
     return out, lse
@@ -841,7 +849,7 @@ def pages_reserve(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     pa = _list(add, "add", S, dev)
     pc, copies = _copies(copies, S, dev)
-    pw, nw, workspace = _scratch(workspace, pages_reserve_workspace_size, (S, num_pages), dev)
+    pw, nw, workspace = _scratch(workspace, pages_reserve_workspace_size, (S, num_pages), dev, stream)
     _launch(load().fa_pages_reserve, dev, stream, *state, pa, pc, S, max_pages, num_pages, int(page_size), pw, nw)
     return copies
 
@@ -880,7 +888,7 @@ def pages_compact(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
     (num_pages // 2, 2), {from, to} and -1 behind the last move, for pages_copy."""
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     pc, copies = _copies(copies, num_pages // 2, dev)
-    pw, nw, workspace = _scratch(workspace, pages_compact_workspace_size, (num_pages,), dev)
+    pw, nw, workspace = _scratch(workspace, pages_compact_workspace_size, (num_pages,), dev, stream)
     _launch(load().fa_pages_compact, dev, stream, *state, pc, S, max_pages, num_pages, int(page_size), pw, nw)
     return copies
 

@@ -243,6 +243,36 @@ def test_many_slots_reserve():
         assert (count.cpu().numpy() == p.ref).all()
 
 
+def test_own_workspace_on_another_stream():
+    """reserve and compact with workspaces of their own on a busy stream, while the current
+    stream allocates and writes as much."""
+    S, ps, mp, N = 300, 16, 20, 4000
+    r = np.random.RandomState(1)
+    p = serving.Pages(S, mp, N, ps)
+    table, lens, count = i32(p.table), i32(p.lens), i32(p.ref)
+    add, gone = r.randint(0, 150, S), np.arange(0, S, 3)
+    side = torch.cuda.Stream()
+    add_d, gone_d = i32(add), i32(gone)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+    c1 = ops.pages_reserve(table, lens, count, add_d, ps, stream=side)
+    ops.pages_free(table, lens, count, gone_d, ps, stream=side)
+    c2 = ops.pages_compact(table, lens, count, ps, stream=side)
+    sizes = [ops.pages_reserve_workspace_size(S, N), ops.pages_compact_workspace_size(N)]
+    fill = [torch.full((n,), 0x11, dtype=torch.uint8, device=DEV) for n in sizes * 4]
+    torch.cuda.current_stream().synchronize()
+    side.synchronize()
+    assert ops.get_error() == ops.FA_OK and len(fill) == 8
+    assert torch.equal(c1.cpu(), torch.from_numpy(p.reserve(add)))
+    p.free(gone)
+    assert torch.equal(c2.cpu(), torch.from_numpy(p.compact()))
+    assert (lens.cpu().numpy() == p.lens).all() and (count.cpu().numpy() == p.ref).all()
+    for s in range(S):
+        h = p.held(p.lens[s])
+        assert (table.cpu().numpy()[s, :h] == p.table[s, :h]).all()
+
+
 @pytest.mark.parametrize("shape,dtype", [((9, 1, 16, 64), torch.uint8), ((7, 3, 48, 64), torch.bfloat16),
                                          ((12, 8, 64, 128), torch.bfloat16), ((600, 2, 16, 128), torch.uint8)])
 def test_copy(shape, dtype):

@@ -290,6 +290,35 @@ def test_two_streams_with_their_own_workspaces():
         assert torch.equal(o, wo) and torch.equal(l, w)
 
 
+@pytest.mark.parametrize("paged", [False, True])
+def test_own_workspace_on_another_stream(paged):
+    """A call that makes its workspace itself, on a stream that is still busy: what the current
+    stream allocates and writes after the call returned must not be that workspace."""
+    n, ps = [400, 129, 800, 33] * 8, 64
+    q, k, v = (t.to(DEV) for t in make(n, n, 8, 2, 128, 43))
+    c = cu(n).to(DEV)
+    if paged:
+        mp = 16
+        table = torch.arange(len(n) * mp, dtype=torch.int32, device=DEV).view(len(n), mp)
+        kp, vp = (torch.randn(len(n) * mp, 2, ps, 128, device=DEV).to(torch.bfloat16) for _ in range(2))
+        lens = torch.tensor(n, dtype=torch.int32, device=DEV)
+    call = lambda **kw: (ops.fwd_varlen_paged(q, kp, vp, table, c, lens, **kw) if paged else
+                         ops.fwd_varlen(q, k, v, c, causal=True, **kw))
+    want, wl = call()
+    o, lse = torch.empty_like(want), torch.empty_like(wl)
+    size = ops.varlen_workspace_size(len(n), sum(n), 8, 2)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some 10 ms
+    call(out=o, lse=lse, stream=side)
+    fill = [torch.full((size,), 0x11, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    torch.cuda.current_stream().synchronize()
+    side.synchronize()
+    assert ops.get_error() == ops.FA_OK and len(fill) == 4
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
 def test_captured_and_replayed_with_other_lengths():
     """The lengths are read on the device: a replay serves whatever the buffers hold then."""
     Hq, Hkv, d, T = 8, 2, 128, 600

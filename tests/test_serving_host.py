@@ -104,6 +104,7 @@ def test_page_calls_reject_the_rest(lib):
     assert lib.fa_pages_copy(FAKE, FAKE, FAKE, 1, 4, 4100, None) == ops.FA_ERR_UNSUPPORTED
     assert lib.fa_pages_copy(FAKE + 8, FAKE, FAKE, 1, 4, 4096, None) == ops.FA_ERR_UNSUPPORTED
     assert lib.fa_pages_copy(FAKE, FAKE, FAKE, 1, 1 << 20, 1 << 30, None) == ops.FA_ERR_UNSUPPORTED
+    assert lib.fa_pages_copy(FAKE, FAKE, FAKE, 1, 1, 1 << 45, None) == ops.FA_ERR_UNSUPPORTED
 
 
 def test_page_workspaces_without_a_gpu(lib):
