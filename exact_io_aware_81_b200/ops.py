@@ -493,7 +493,8 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
 # These calls are short (a few microseconds on the device), so their checks come in two parts:
 # one expression that a right argument passes (devices compared by index), and, when it does not,
 # a function that finds out what is wrong.  The device is switched only when the tensors are not
-# on the current one.
+# on the current one.  With stream=, what a call makes itself is that stream's memory (_new); what
+# the caller passes is the caller's to keep until the call has run.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without an object
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -572,19 +573,28 @@ def _launch(fn, dev, stream, *args):
         _check(rc)
 
 
+def _new(shape, dtype, dev, stream, handed_back=True):
+    """A tensor that a call makes: memory of the stream that the call runs on.  As memory of the
+    current stream it could be handed out while other work of that stream still used it, and handed
+    out again, once dropped, before the call had run.  One that is handed back to the caller may be
+    used on the current stream too, so that stream is recorded as a user."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    current = torch.cuda.current_stream(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if handed_back:
+        t.record_stream(current)
+    return t
+
+
 def _scratch(workspace, size, sizes, dev, stream):
     """(pointer, bytes) of the caller's workspace, whose size the library checks, or of a new one of
-    size(*sizes) bytes (kept alive by the third).  A new one is memory of the stream that the call
-    runs on: it is given back when the call returns, and only work behind it may use it again."""
+    size(*sizes) bytes (kept alive by the third)."""
     if workspace is None:
-        n = max(size(*sizes), 16)
-        if stream is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream.cuda_stream), dev)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = _new(max(size(*sizes), 16), torch.uint8, dev, stream, handed_back=False)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     elif workspace.get_device() != dev:
@@ -619,15 +629,15 @@ def varlen_workspace_size(B: int, Tq: int, Hq: int, Hkv: int) -> int:
     return int(load().fa_fwd_varlen_workspace_size(B, Tq, Hq, Hkv))
 
 
-def _varlen_outputs(q, dev, out_dtype, out, lse):
+def _varlen_outputs(q, dev, out_dtype, out, lse, stream):
     """Pointers of o (Tq,Hq,d) and lse (Hq,Tq), new ones unless given, and the output's code."""
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be bfloat16 or float32")
     Tq, Hq, d = q.shape
     if out is None:
-        out = torch.empty((Tq, Hq, d), dtype=out_dtype, device=dev)
+        out = _new((Tq, Hq, d), out_dtype, dev, stream)
     if lse is None:
-        lse = torch.empty((Hq, Tq), dtype=torch.float32, device=dev)
+        lse = _new((Hq, Tq), torch.float32, dev, stream)
     po, pl = _tensor(out, "out", out_dtype, 3, dev), _tensor(lse, "lse", torch.float32, 2, dev)
     if out.shape != q.shape or tuple(lse.shape) != (Hq, Tq):
         raise ValueError(f"out must have shape {tuple(q.shape)} and lse {(Hq, Tq)}, "
@@ -654,7 +664,7 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
     if (dk != d or (Tv, Hv, dv) != (Tk, Hkv, dk) or B < 1
             or (cu_seqlens_k is not None and cu_seqlens_k.numel() != B + 1)):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)} v {tuple(v.shape)} and the cu_seqlens")
-    po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse)
+    po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if Tq == 0:
@@ -684,7 +694,7 @@ def fwd_varlen_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
     B, max_pages = block_table.shape
     if dk != d or vpages.shape != kpages.shape or seqlens.shape[0] != B or cu_seqlens_q.shape[0] != B + 1:
         raise ValueError("shape mismatch between q, kpages, vpages, block_table, cu_seqlens_q and seqlens")
-    po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse)
+    po, pl, out, lse, odt = _varlen_outputs(q, dev, out_dtype, out, lse, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if Tq == 0:
@@ -714,10 +724,10 @@ def rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.
         raise ValueError("q and k must have the same tokens and head dim")
     T, d = (Tq, dq) if q is not None else (Tk, dk)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _new(q.shape, q.dtype, dev, stream)
         pqo, sqo = q_out.data_ptr(), Hq * dq
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = _new(k.shape, k.dtype, dev, stream)
         pko, sko = k_out.data_ptr(), Hk * dk
     if q is None:
         q_out = None
@@ -794,7 +804,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
     sq = so = Hq = 0
     if q is not None:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+            q_out = _new(q.shape, torch.bfloat16, dev, stream)
         pq, sq, po, so, Tq, Hq, dq = _turned(q, q_out, "q", _BF16, dev)
         if (Tq, dq) != (T, d):
             raise ValueError("q and k must have the same tokens and head dim")
@@ -823,9 +833,9 @@ def _list(t, name, n, dev):
     return p
 
 
-def _copies(copies, n, dev):
+def _copies(copies, n, dev, stream):
     if copies is None:
-        copies = torch.empty((n, 2), dtype=torch.int32, device=dev)
+        copies = _new((n, 2), torch.int32, dev, stream)
     p = _tensor(copies, "copies", torch.int32, 2, dev)
     if tuple(copies.shape) != (n, 2):
         raise ValueError(f"copies must have shape {(n, 2)}, got {tuple(copies.shape)}")
@@ -848,7 +858,7 @@ def pages_reserve(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
     every layer's pools.  Too few free pages: nothing changes, get_error() says so."""
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     pa = _list(add, "add", S, dev)
-    pc, copies = _copies(copies, S, dev)
+    pc, copies = _copies(copies, S, dev, stream)
     pw, nw, workspace = _scratch(workspace, pages_reserve_workspace_size, (S, num_pages), dev, stream)
     _launch(load().fa_pages_reserve, dev, stream, *state, pa, pc, S, max_pages, num_pages, int(page_size), pw, nw)
     return copies
@@ -887,7 +897,7 @@ def pages_compact(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
     """Move the live pages to the front of the pool (fa_pages_compact).  Returns copies int32
     (num_pages // 2, 2), {from, to} and -1 behind the last move, for pages_copy."""
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
-    pc, copies = _copies(copies, num_pages // 2, dev)
+    pc, copies = _copies(copies, num_pages // 2, dev, stream)
     pw, nw, workspace = _scratch(workspace, pages_compact_workspace_size, (num_pages,), dev, stream)
     _launch(load().fa_pages_compact, dev, stream, *state, pc, S, max_pages, num_pages, int(page_size), pw, nw)
     return copies
