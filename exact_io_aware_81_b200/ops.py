@@ -5,6 +5,10 @@ dtype and contiguity, passes their device pointers and the current CUDA stream t
 library, and raises ``FAError`` with the library's status and message on failure.  No
 attention arithmetic happens in Python; if ``libfa.so`` has not been built, every call
 raises instead of falling back to anything else.
+
+Calls run on the current stream, or on ``stream``.  Tensors that a call on another stream makes
+itself are that stream's memory; those that the caller passes are the caller's to keep until the
+call has run.
 """
 from __future__ import annotations
 
@@ -141,11 +145,28 @@ def _require(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _output(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device) -> torch.Tensor:
+def _new(shape, dtype, dev, stream, handed_back=True):
+    """A tensor that a call makes: memory of the stream that the call runs on.  As memory of the
+    current stream it could be handed out while other work of that stream still used it, and handed
+    out again, once dropped, before the call had run.  One that is handed back to the caller may be
+    used on the current stream too, so that stream is recorded as a user."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    current = torch.cuda.current_stream(dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if handed_back:
+        t.record_stream(current)
+    return t
+
+
+def _output(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device, stream) -> torch.Tensor:
     """A caller-provided output checked against its dtype and exact shape, or a new one."""
     shape = tuple(shape)
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device, stream)
     _require(t, name, dtype, len(shape))
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
@@ -175,7 +196,7 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
         scale = 1.0 / math.sqrt(d)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be bfloat16 or float32")
-    out, lse = _fwd_outputs(q, (B, Hq, Nq, d), (B, Hq, Nq), out_dtype, out, lse)
+    out, lse = _fwd_outputs(q, (B, Hq, Nq, d), (B, Hq, Nq), out_dtype, out, lse, stream)
     odt = FA_F32 if out_dtype == torch.float32 else FA_BF16
     if window:
         if not causal:
@@ -193,9 +214,9 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
     return out, lse
 
 
-def _fwd_outputs(q, o_shape, lse_shape, out_dtype, out, lse):
-    return (_output(out, "out", out_dtype, o_shape, q.device),
-            _output(lse, "lse", torch.float32, lse_shape, q.device))
+def _fwd_outputs(q, o_shape, lse_shape, out_dtype, out, lse, stream):
+    return (_output(out, "out", out_dtype, o_shape, q.device, stream),
+            _output(lse, "lse", torch.float32, lse_shape, q.device, stream))
 
 
 def fwd_bshd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
@@ -218,7 +239,7 @@ def fwd_bshd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = F
         raise ValueError("out_dtype must be bfloat16 or float32")
     if window and not causal:
         raise ValueError("a sliding window needs causal=True")
-    out, lse = _fwd_outputs(q, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, out, lse)
+    out, lse = _fwd_outputs(q, (B, Nq, Hq, d), (B, Hq, Nq), out_dtype, out, lse, stream)
     odt = FA_F32 if out_dtype == torch.float32 else FA_BF16
     with _on_device(q, k, v, out, lse) as dev:
         rc = load().fa_fwd_bshd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -263,7 +284,7 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: torch.Te
         scale = 1.0 / math.sqrt(d)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be bfloat16 or float32")
-    out, lse = _fwd_outputs(q, (B, Hq, Nq, d), (B, Hq, Nq), out_dtype, out, lse)
+    out, lse = _fwd_outputs(q, (B, Hq, Nq, d), (B, Hq, Nq), out_dtype, out, lse, stream)
     odt = FA_F32 if out_dtype == torch.float32 else FA_BF16
     with _on_device(q, k, v, q_scale, k_scale, v_scale, out, lse) as dev:
         rc = load().fa_fwd_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_scale.data_ptr(),
@@ -297,12 +318,8 @@ def decode(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, seqlens:
         raise ValueError("shape mismatch between q, kcache, vcache and seqlens")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = decode_workspace_size(B, Hq, Nmax, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    out, lse = _decode_outputs(q, out, lse, want_lse)
+    workspace = _workspace(workspace, decode_workspace_size(B, Hq, Nmax, d), q.device, stream)
+    out, lse = _decode_outputs(q, out, lse, want_lse, stream)
     with _on_device(q, kcache, vcache, seqlens, out, lse, workspace) as dev:
         rc = load().fa_decode(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), seqlens.data_ptr(),
                               out.data_ptr(), lse.data_ptr() if lse is not None else None,
@@ -333,12 +350,8 @@ def decode_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor,
         raise ValueError("shape mismatch between q, kpages, vpages, block_table and seqlens")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    need = decode_workspace_size(B, Hq, page_size * max_pages, d)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    out, lse = _decode_outputs(q, out, lse, want_lse)
+    workspace = _workspace(workspace, decode_workspace_size(B, Hq, page_size * max_pages, d), q.device, stream)
+    out, lse = _decode_outputs(q, out, lse, want_lse, stream)
     with _on_device(q, kpages, vpages, block_table, seqlens, out, lse, workspace) as dev:
         rc = load().fa_decode_paged(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
                                     block_table.data_ptr(), seqlens.data_ptr(), out.data_ptr(),
@@ -350,17 +363,17 @@ def decode_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor,
     return out, lse
 
 
-def _decode_outputs(q, out, lse, want_lse, out_dtype=torch.bfloat16):
+def _decode_outputs(q, out, lse, want_lse, stream, out_dtype=torch.bfloat16):
     B, Hq, d = q.shape
-    out = _output(out, "out", out_dtype, (B, Hq, d), q.device)
+    out = _output(out, "out", out_dtype, (B, Hq, d), q.device, stream)
     if lse is not None or want_lse:
-        lse = _output(lse, "lse", torch.float32, (B, Hq), q.device)
+        lse = _output(lse, "lse", torch.float32, (B, Hq), q.device, stream)
     return out, lse
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, device, stream):
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return _new(max(need, 16), torch.uint8, device, stream, handed_back=False)
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     return workspace
@@ -384,8 +397,8 @@ def decode_ex(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, seqle
         raise ValueError("out_dtype must be bfloat16 or float32")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    workspace = _workspace(workspace, decode_workspace_size(B, Hq, Nmax, d), q.device)
-    out, lse = _decode_outputs(q, out, lse, want_lse, out_dtype)
+    workspace = _workspace(workspace, decode_workspace_size(B, Hq, Nmax, d), q.device, stream)
+    out, lse = _decode_outputs(q, out, lse, want_lse, stream, out_dtype)
     with _on_device(q, kcache, vcache, seqlens, out, lse, workspace) as dev:
         rc = load().fa_decode_ex(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), seqlens.data_ptr(),
                                  out.data_ptr(), lse.data_ptr() if lse is not None else None,
@@ -411,8 +424,8 @@ def merge_lse(o_parts: torch.Tensor, lse_parts: torch.Tensor, out_dtype: torch.d
         rows *= x
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("out_dtype must be bfloat16 or float32")
-    out = _output(out, "out", out_dtype, row_shape + (d,), o_parts.device)
-    lse = _output(lse, "lse", torch.float32, row_shape, o_parts.device)
+    out = _output(out, "out", out_dtype, row_shape + (d,), o_parts.device, stream)
+    lse = _output(lse, "lse", torch.float32, row_shape, o_parts.device, stream)
     with _on_device(o_parts, lse_parts, out, lse) as dev:
         rc = load().fa_merge_lse(o_parts.data_ptr(), lse_parts.data_ptr(), P, rows, d, out.data_ptr(),
                                  lse.data_ptr(), FA_F32 if out_dtype == torch.float32 else FA_BF16,
@@ -440,8 +453,8 @@ def decode_fp8(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor, k_sc
         raise ValueError("shape mismatch between q, the caches, the scales and seqlens")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    workspace = _workspace(workspace, decode_workspace_size(B, Hq, Nmax, d), q.device)
-    out, lse = _decode_outputs(q, out, lse, want_lse)
+    workspace = _workspace(workspace, decode_workspace_size(B, Hq, Nmax, d), q.device, stream)
+    out, lse = _decode_outputs(q, out, lse, want_lse, stream)
     with _on_device(q, kcache, vcache, k_scale, v_scale, seqlens, out, lse, workspace) as dev:
         rc = load().fa_decode_fp8(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), k_scale.data_ptr(),
                                   v_scale.data_ptr(), seqlens.data_ptr(), out.data_ptr(),
@@ -474,8 +487,8 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
         raise ValueError("shape mismatch between q, the pools, the scales, block_table and seqlens")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    workspace = _workspace(workspace, decode_workspace_size(B, Hq, page_size * max_pages, d), q.device)
-    out, lse = _decode_outputs(q, out, lse, want_lse)
+    workspace = _workspace(workspace, decode_workspace_size(B, Hq, page_size * max_pages, d), q.device, stream)
+    out, lse = _decode_outputs(q, out, lse, want_lse, stream)
     with _on_device(q, kpages, vpages, k_scale, v_scale, block_table, seqlens, out, lse, workspace) as dev:
         rc = load().fa_decode_paged_fp8(q.data_ptr(), kpages.data_ptr(), vpages.data_ptr(),
                                         k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
@@ -493,8 +506,7 @@ def decode_paged_fp8(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
 # These calls are short (a few microseconds on the device), so their checks come in two parts:
 # one expression that a right argument passes (devices compared by index), and, when it does not,
 # a function that finds out what is wrong.  The device is switched only when the tensors are not
-# on the current one.  With stream=, what a call makes itself is that stream's memory (_new); what
-# the caller passes is the caller's to keep until the call has run.
+# on the current one.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # current_stream without an object
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -571,23 +583,6 @@ def _launch(fn, dev, stream, *args):
             rc = fn(*args, handle)
     if rc != FA_OK:
         _check(rc)
-
-
-def _new(shape, dtype, dev, stream, handed_back=True):
-    """A tensor that a call makes: memory of the stream that the call runs on.  As memory of the
-    current stream it could be handed out while other work of that stream still used it, and handed
-    out again, once dropped, before the call had run.  One that is handed back to the caller may be
-    used on the current stream too, so that stream is recorded as a user."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    current = torch.cuda.current_stream(dev)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream.cuda_stream), dev)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-    if handed_back:
-        t.record_stream(current)
-    return t
 
 
 def _scratch(workspace, size, sizes, dev, stream):
@@ -940,8 +935,7 @@ def fwd_selftest_timeout(q, k, v, causal=False, scale=None, stream=None):
     Hkv, Nk = k.shape[1], k.shape[2]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+    out, lse = _fwd_outputs(q, (B, Hq, Nq, d), (B, Hq, Nq), torch.bfloat16, None, None, stream)
     with _on_device(q, k, v, out, lse) as dev:
         rc = load().fa_fwd_selftest_timeout(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                             lse.data_ptr(), B, Hq, Hkv, Nq, Nk, d, float(scale),
@@ -957,9 +951,8 @@ def decode_selftest_timeout(q, kcache, vcache, seqlens, k_scale=None, v_scale=No
     Hkv, Nmax = kcache.shape[1], kcache.shape[2]
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    ws = torch.empty(decode_workspace_size(B, Hq, Nmax, d), dtype=torch.uint8, device=q.device)
+    out, lse = _decode_outputs(q, None, None, True, stream)
+    ws = _workspace(None, decode_workspace_size(B, Hq, Nmax, d), q.device, stream)
     with _on_device(q, kcache, vcache, seqlens, out, lse, ws, k_scale, v_scale) as dev:
         rc = load().fa_decode_selftest_timeout(
             q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
@@ -994,7 +987,7 @@ def decode_noalloc(q: torch.Tensor, kcache: torch.Tensor, vcache: torch.Tensor,
         scale = 1.0 / math.sqrt(d)
     if out is None:
         raise ValueError("decode_noalloc writes into a caller-provided `out`")
-    out, lse = _decode_outputs(q, out, lse, False)
+    out, lse = _decode_outputs(q, out, lse, False, stream)
     with _on_device(q, kcache, vcache, seqlens, out, lse) as dev:
         rc = load().fa_decode_noalloc(q.data_ptr(), kcache.data_ptr(), vcache.data_ptr(),
                                       seqlens.data_ptr(), out.data_ptr(),

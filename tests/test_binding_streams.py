@@ -118,3 +118,32 @@ def check(made, call):
 @pytest.mark.parametrize("name", ["fwd_varlen", "fwd_varlen_paged", "rope", "rope_append", "pages_reserve", "pages_compact"])
 def test_what_a_serving_call_makes_is_its_streams_memory(made, name):
     check(made, serving_calls()[name])
+
+
+def dense_calls():
+    q, k = gpu(2, 4, 8, 128), gpu(2, 2, 8, 128)
+    q8, k8, s4, s2 = gpu(2, 4, 8, 128, dtype=u8), gpu(2, 2, 8, 128, dtype=u8), gpu(4, dtype=f32), gpu(2, dtype=f32)
+    qd, sl, pages, table = gpu(2, 4, 128), gpu(2, dtype=i32), gpu(6, 2, 16, 128), gpu(2, 3, dtype=i32)
+    pages8 = gpu(6, 2, 16, 128, dtype=u8)
+    bshd = lambda t: t.transpose(1, 2).contiguous().as_subclass(OnGpu)  # noqa: E731
+    return {
+        "fwd": lambda **kw: ops.fwd(q, k, k, **kw),
+        "fwd_bshd": lambda **kw: ops.fwd_bshd(bshd(q), bshd(k), bshd(k), **kw),
+        "fwd_window": lambda **kw: ops.fwd_window(q, k, k, 4, **kw),
+        "fwd_fp8": lambda **kw: ops.fwd_fp8(q8, k8, k8, s4, s2, s2, **kw),
+        "decode": lambda **kw: ops.decode(qd, k, k, sl, **kw),
+        "decode_ex": lambda **kw: ops.decode_ex(qd, k, k, sl, **kw),
+        "decode_paged": lambda **kw: ops.decode_paged(qd, pages, pages, table, sl, **kw),
+        "decode_fp8": lambda **kw: ops.decode_fp8(qd, k8, k8, s2, s2, sl, **kw),
+        "decode_paged_fp8": lambda **kw: ops.decode_paged_fp8(qd, pages8, pages8, s2, s2, table, sl, **kw),
+        "merge_lse": lambda **kw: ops.merge_lse(gpu(3, 2, 4, 64, dtype=f32), gpu(3, 2, 4, dtype=f32), **kw),
+        "fwd_selftest_timeout": lambda **kw: ops.fwd_selftest_timeout(q, k, k, **kw),
+        "decode_selftest_timeout": lambda **kw: ops.decode_selftest_timeout(qd, k, k, sl, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", ["fwd", "fwd_bshd", "fwd_window", "fwd_fp8", "decode", "decode_ex", "decode_paged",
+                                  "decode_fp8", "decode_paged_fp8", "merge_lse", "fwd_selftest_timeout",
+                                  "decode_selftest_timeout"])
+def test_what_a_dense_or_decode_call_makes_is_its_streams_memory(made, name):
+    check(made, dense_calls()[name])

@@ -113,3 +113,21 @@ def test_a_raw_stream_and_the_current_one():
     b = ops.rope(q, None, pos, inv, stream=torch.cuda.current_stream())[0]
     torch.cuda.synchronize()
     assert torch.equal(a, want) and torch.equal(b, want) and ops.get_error() == ops.FA_OK
+
+
+def test_decode_workspace_and_outputs_on_a_busy_stream():
+    """The decode's partial results lie in a workspace that nobody holds once the call has returned."""
+    B, Hq, Hkv, N, d = 4, 8, 2, 5000, 128
+    q, kc, vc = randn(B, Hq, d), randn(B, Hkv, N, d, seed=1), randn(B, Hkv, N, d, seed=2)
+    sl = i32([5000, 1, 3000, 777])
+    want, wl = ops.decode(q, kc, vc, sl)
+    x, k, v = randn(2, Hq, 600, d, seed=3), randn(2, Hkv, 600, d, seed=4), randn(2, Hkv, 600, d, seed=5)
+    wx, wxl = ops.fwd(x, k, v, causal=True)
+    busy = busy_stream()
+    o = ops.decode(q, kc, vc, sl, stream=busy)[0]
+    lse = ops.decode(q, kc, vc, sl, stream=busy)[1]
+    xo = ops.fwd(x, k, v, causal=True, stream=busy)[0]
+    xl = ops.fwd(x, k, v, causal=True, stream=busy)[1]
+    intact = fill_like([ops.decode_workspace_size(B, Hq, N, d), 2 * B * Hq * d, 4 * B * Hq, wx.numel() * 2, wxl.numel() * 4])
+    assert intact() and ops.get_error() == ops.FA_OK
+    assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(xo, wx) and torch.equal(xl, wxl)
