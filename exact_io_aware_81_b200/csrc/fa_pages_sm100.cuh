@@ -56,8 +56,10 @@ __device__ __forceinline__ bool len_ok(const PageTables &t, int len)
     return len >= 0 && (long long)len <= (long long)t.page_size * t.max_pages;
 }
 
-// Exclusive prefix sum over the CTA (kPlanThreads); `total` is the sum over all threads.
-__device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums)
+// Exclusive prefix sum over the CTA (kPlanThreads); `total` is the sum over all threads.  A warp
+// counts for `most` at most: where no prefix passes `most` that changes nothing, and prefixes
+// that pass it stay above it, whatever the true sum, while 32 warps cannot overflow an int.
+__device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums, int most = 0x7fffffff)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int x = v;
@@ -67,7 +69,7 @@ __device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums)
         if (lane >= off) x += y;
     }
     __syncthreads();  // warp_sums of the previous call has been read
-    if (lane == 31) warp_sums[warp] = x;
+    if (lane == 31) warp_sums[warp] = min(x, most);
     __syncthreads();
     int w = warp_sums[lane];  // kPlanThreads / 32 = 32 warps
 #pragma unroll

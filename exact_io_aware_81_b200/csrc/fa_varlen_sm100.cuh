@@ -126,6 +126,9 @@ __global__ void __launch_bounds__(varlen::kThreads, 1) fa_varlen_plan_kernel(con
     if (tid == 0) top = 1;
     for (int i = tid; i < kBins; i += kThreads) bins[i] = 0;
 
+    // Sequences that overlap (cu_q that does not ascend) can ask for more jobs than the plan holds,
+    // and than an int does: counts, sums and `first` stop at one job more than that.
+    const int most = p.max_jobs + 1;  // (2^26 / 8 + 4096 at most: 32 of them stay below 2^29)
     bool bad = false;
     int n_jobs = 0, longest = 1;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -133,16 +136,15 @@ __global__ void __launch_bounds__(varlen::kThreads, 1) fa_varlen_plan_kernel(con
         int n = 0;
         if (b < p.B) {
             const Seq s = sequence(p, b, bad);
-            n = (s.nq + p.rows - 1) / p.rows;
+            n = min((s.nq + p.rows - 1) / p.rows, most);
             longest = max(longest, (s.nk + 127) / 128);
         }
         int sum;
-        const int at = pages::block_scan(n, sum, warp_sums);
-        if (b < p.B) first[b] = n_jobs + at;
-        n_jobs += sum;
+        const int at = pages::block_scan(n, sum, warp_sums, most);
+        if (b < p.B) first[b] = min(n_jobs + at, most);
+        n_jobs = min(n_jobs + sum, most);
     }
     if (tid == 0) first[p.B] = n_jobs;
-    // sequences that overlap could ask for more jobs than the plan holds
     if (n_jobs > p.max_jobs) {
         bad = true;
         n_jobs = p.max_jobs;

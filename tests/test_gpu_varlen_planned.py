@@ -276,3 +276,32 @@ def test_the_restated_rule_names_the_kernel_that_runs():
             assert any("fa_varlen_plan_kernel" in n for n in names) == (kind != WAVE)
     if not seen:
         pytest.skip("the profiler reports no kernels here")
+
+
+def test_more_jobs_than_an_int_counts():
+    """cu_seqlens that go back to 0 again and again: 2048 sequences of 2^20 jobs each, 2^31 in all.
+    The plan stops at what it holds (2^20 + 4096 jobs: the first sequence and a bit of the next),
+    and reports.  In 32 bits the sum would wrap, and jobs start at negative rows."""
+    Hq, Hkv, d, B, T = 32, 1, 64, 4096, 1 << 23
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 70 GB of device memory")
+    q = torch.zeros(T, Hq, d, dtype=torch.bfloat16, device=DEV)
+    o = torch.full_like(q, SENTINEL)
+    lse = torch.full((Hq, T), SENTINEL, device=DEV)
+    v = torch.arange(1, d + 1, device=DEV).to(torch.bfloat16).view(1, 1, d)
+    cq = torch.zeros(B + 1, dtype=torch.int32, device=DEV)
+    cq[1::2] = T
+    ck = torch.ones(B + 1, dtype=torch.int32, device=DEV)
+    ck[0] = 0   # one key, of the first sequence
+    ws = torch.full((ops.varlen_workspace_size(B, T, Hq, Hkv),), 0xFF, dtype=torch.uint8, device=DEV)
+    ops.fwd_varlen(q, v, v, cq, ck, workspace=ws, out=o, lse=lse)
+    assert ops.get_error() == ops.FA_ERR_DEVICE_ARG
+    assert int(ws[:4].view(torch.int32)) == T // 8 + B
+    n = 8 * B   # rows that the second whole sequence (without keys) has too
+    for a in range(0, T, T // 16):
+        part, z = o[a:a + T // 16], lse[:, a:a + T // 16]
+        ok, oz = (part == v).all(-1), z == 0
+        if a == 0:
+            ok[:n] |= (part[:n] == 0).all(-1)
+            oz[:, :n] |= z[:, :n] == -math.inf
+        assert ok.all() and oz.all()
