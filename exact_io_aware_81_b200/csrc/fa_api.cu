@@ -771,7 +771,7 @@ namespace {
 struct PageDest {
     void *k, *v;
     const float *k_scale, *v_scale;
-    const int *block_table, *cu_seqlens, *seqlens;
+    const int *block_table, *cu_seqlens, *seqlens, *status;
     int B, num_pages, page_size, max_pages;
 };
 
@@ -854,6 +854,7 @@ int rope_general(fa::RopeParams &p, const PageDest *pages, int d, int dtype, voi
         p.block_table = pages->block_table;
         p.cu_seqlens = pages->cu_seqlens;
         p.seqlens = pages->seqlens;
+        p.status = pages->status;
         p.B = pages->B;
         p.num_pages = pages->num_pages;
         p.page_size = pages->page_size;
@@ -1189,12 +1190,12 @@ int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const int *p
     return rope_general(p, nullptr, d, dtype, stream);
 }
 
-int fa_rope_append(const void *q, const void *k, const void *v, void *q_out, const int *positions,
-                   const float *inv_freq, const int *axes, void *kpages, void *vpages, const float *k_scale,
-                   const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens, int T,
-                   int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages, int d, int F, int A,
-                   long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
-                   int interleaved, void *stream)
+int fa_rope_append_ex(const void *q, const void *k, const void *v, void *q_out, const int *positions,
+                      const float *inv_freq, const int *axes, void *kpages, void *vpages, const float *k_scale,
+                      const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens,
+                      const int *status, int T, int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages,
+                      int d, int F, int A, long long q_stride, long long k_stride, long long v_stride,
+                      long long q_out_stride, int interleaved, void *stream)
 {
     if (!inv_freq) return fail(FA_ERR_INVALID, "null pointer argument");
     fa::RopeParams p;
@@ -1204,7 +1205,34 @@ int fa_rope_append(const void *q, const void *k, const void *v, void *q_out, con
     p.positions = positions, p.inv_freq = inv_freq, p.axes = axes;
     p.T = T, p.Hq = Hq, p.Hkv = Hkv, p.F = F, p.A = A;
     p.interleaved = interleaved ? 1 : 0;
-    const PageDest dest{kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, B, num_pages, page_size, max_pages};
+    const PageDest dest{kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, status, B, num_pages,
+                        page_size, max_pages};
+    return rope_general(p, &dest, d, FA_BF16, stream);
+}
+
+int fa_rope_append(const void *q, const void *k, const void *v, void *q_out, const int *positions,
+                   const float *inv_freq, const int *axes, void *kpages, void *vpages, const float *k_scale,
+                   const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens, int T,
+                   int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages, int d, int F, int A,
+                   long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
+                   int interleaved, void *stream)
+{
+    return fa_rope_append_ex(q, k, v, q_out, positions, inv_freq, axes, kpages, vpages, k_scale, v_scale, block_table,
+                             cu_seqlens, seqlens, nullptr, T, B, Hq, Hkv, num_pages, page_size, max_pages, d, F, A,
+                             q_stride, k_stride, v_stride, q_out_stride, interleaved, stream);
+}
+
+int fa_cache_append_ex(const void *k, const void *v, void *kpages, void *vpages, const float *k_scale,
+                       const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens,
+                       const int *status, int T, int B, int Hkv, int num_pages, int page_size, int max_pages, int d,
+                       long long k_stride, long long v_stride, void *stream)
+{
+    fa::RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.k = k, p.v = v, p.k_s = k_stride, p.v_s = v_stride;
+    p.T = T, p.Hkv = Hkv;
+    const PageDest dest{kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, status, B, num_pages,
+                        page_size, max_pages};
     return rope_general(p, &dest, d, FA_BF16, stream);
 }
 
@@ -1213,12 +1241,8 @@ int fa_cache_append(const void *k, const void *v, void *kpages, void *vpages, co
                     int B, int Hkv, int num_pages, int page_size, int max_pages, int d, long long k_stride,
                     long long v_stride, void *stream)
 {
-    fa::RopeParams p;
-    memset(&p, 0, sizeof p);
-    p.k = k, p.v = v, p.k_s = k_stride, p.v_s = v_stride;
-    p.T = T, p.Hkv = Hkv;
-    const PageDest dest{kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, B, num_pages, page_size, max_pages};
-    return rope_general(p, &dest, d, FA_BF16, stream);
+    return fa_cache_append_ex(k, v, kpages, vpages, k_scale, v_scale, block_table, cu_seqlens, seqlens, nullptr, T, B,
+                              Hkv, num_pages, page_size, max_pages, d, k_stride, v_stride, stream);
 }
 
 // ------------------------------------------------------------------ page management
@@ -1255,8 +1279,9 @@ int fa_pages_free(int *block_table, int *seqlens, int *refcount, const int *slot
 
 size_t fa_pages_reserve_workspace_size(int S, int num_pages) { return reserve_ws_bytes(S, num_pages); }
 
-int fa_pages_reserve(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int S, int max_pages,
-                     int num_pages, int page_size, void *workspace, size_t workspace_bytes, void *stream)
+int fa_pages_reserve_ex(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int *status, int S,
+                        int max_pages, int num_pages, int page_size, void *workspace, size_t workspace_bytes,
+                        void *stream)
 {
     if (!add || !copies) return fail(FA_ERR_INVALID, "null pointer argument");
     fa::ReserveParams p;
@@ -1264,11 +1289,18 @@ int fa_pages_reserve(int *block_table, int *seqlens, int *refcount, const int *a
     int rc = make_tables(&p.t, block_table, seqlens, refcount, S, max_pages, num_pages, page_size, &info);
     if (rc != FA_OK) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, reserve_ws_bytes(S, num_pages))) != FA_OK) return rc;
-    p.add = add, p.copies = copies;
+    p.add = add, p.copies = copies, p.status = status;
     p.first = static_cast<int *>(workspace);
     p.free_ids = reinterpret_cast<int *>(static_cast<char *>(workspace) + align256((size_t)S * 4));
     fa::fa_pages_reserve_kernel<<<1, fa::pages::kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return launched("reserve");
+}
+
+int fa_pages_reserve(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int S, int max_pages,
+                     int num_pages, int page_size, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return fa_pages_reserve_ex(block_table, seqlens, refcount, add, copies, nullptr, S, max_pages, num_pages, page_size,
+                               workspace, workspace_bytes, stream);
 }
 
 size_t fa_pages_compact_workspace_size(int num_pages) { return compact_ws_bytes(num_pages); }

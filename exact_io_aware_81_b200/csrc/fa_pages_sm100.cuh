@@ -29,6 +29,7 @@
 
 #include <cstdint>
 
+#include "fa.h"
 #include "fa_common.cuh"
 
 namespace fa {
@@ -188,6 +189,7 @@ struct ReserveParams {
     PageTables t;
     const int *add;   // (S)
     int *copies;      // (S, 2)
+    int *status;      // (1) or null: what became of the call
     int *first;       // workspace (S): place of a slot's pages in free_ids
     int *free_ids;    // workspace (num_pages)
 };
@@ -279,10 +281,14 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_reserve_kerne
         }
     }
     if (bad || found < total) {
-        if (tid == 0) raise_error(bad ? kErrSlot : kErrNoPages);
+        if (tid == 0) {
+            if (bad || !p.status) raise_error(bad ? kErrSlot : kErrNoPages);
+            if (p.status) *p.status = bad ? FA_ERR_DEVICE_ARG : FA_ERR_NO_PAGES;
+        }
         for (int s = tid; s < 2 * p.t.S; s += kPlanThreads) p.copies[s] = -1;
         return;
     }
+    if (p.status && tid == 0) *p.status = FA_OK;
     __syncthreads();  // free_ids is complete
 
     // The sums decided on the refcounts at the start of the call, and this pass lowers some of

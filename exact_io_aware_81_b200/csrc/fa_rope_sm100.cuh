@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include "fa.h"
 #include "fa_common.cuh"
 
 namespace fa {
@@ -47,6 +48,7 @@ struct RopeParams {
     const int *block_table;  // (B, max_pages)
     const int *cu_seqlens;   // (B + 1)
     const int *seqlens;      // (B): lengths that include these tokens
+    const int *status;       // (1) or null: not FA_OK, the lengths do not include them and nothing is written
     int B, num_pages, page_size, max_pages;
 };
 
@@ -139,6 +141,10 @@ __device__ __forceinline__ int sequence_of(const int *cu, int B, int t)
     return lo;
 }
 
+// Did the reservation that the tokens need not take place?  Their positions are then those of
+// finished tokens, perhaps in shared pages.
+__device__ __forceinline__ bool refused(const RopeParams &p) { return p.status && *p.status != FA_OK; }
+
 // Where token t's k and v go: row = page * Hkv * page_size + the row in the page, or -1 (and
 // an error recorded) when the lengths or the block table do not hold the token.  False for a
 // token behind the last sequence, of which nothing is written.  Whole warp.
@@ -183,6 +189,7 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
     __shared__ float4 cos_t[ROT ? kTokens : 1][QV][LANES], sin_t[ROT ? kTokens : 1][QV][LANES];
     __shared__ long long page_rows[kTokens];
 
+    if (PAGES && refused(p)) return;
     const int tid = threadIdx.x;
     const int part = blockIdx.x % p.split;
     const int t0 = (int)(blockIdx.x / p.split) * p.tokens;
@@ -335,6 +342,7 @@ template <int D, typename T, bool PAGES, bool FP8>
 __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const RopeParams p)
 {
     using namespace rope;
+    if (PAGES && refused(p)) return;
     const int lane = threadIdx.x & 31;
     const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int n_rows = p.Hq + p.Hkv + (PAGES ? p.Hkv : 0);

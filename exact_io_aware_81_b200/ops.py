@@ -58,9 +58,12 @@ SIGNATURES = {
     "fa_fwd_varlen_paged": (_I, [_P] * 8 + [_I] * 8 + [_L, _F, _I, _I, _I, _P, _Z, _P]),
     "fa_rope": (_I, [_P] * 7 + [_I] * 6 + [_L] * 4 + [_I] * 3 + [_P]),
     "fa_cache_append": (_I, [_P] * 9 + [_I] * 7 + [_L] * 2 + [_P]),
+    "fa_cache_append_ex": (_I, [_P] * 10 + [_I] * 7 + [_L] * 2 + [_P]),
     "fa_rope_append": (_I, [_P] * 14 + [_I] * 10 + [_L] * 4 + [_I, _P]),
+    "fa_rope_append_ex": (_I, [_P] * 15 + [_I] * 10 + [_L] * 4 + [_I, _P]),
     "fa_pages_reserve_workspace_size": (_Z, [_I, _I]),
     "fa_pages_reserve": (_I, [_P] * 5 + [_I] * 4 + [_P, _Z, _P]),
+    "fa_pages_reserve_ex": (_I, [_P] * 6 + [_I] * 4 + [_P, _Z, _P]),
     "fa_pages_fork": (_I, [_P] * 6 + [_I] * 5 + [_P]),
     "fa_pages_free": (_I, [_P] * 5 + [_I] * 5 + [_P]),
     "fa_pages_compact_workspace_size": (_Z, [_I]),
@@ -749,7 +752,17 @@ def _turned(x, out, name, types, dev):
     return p, st, po, so, T, H, d
 
 
-def _destination(k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev):
+def _status(status, dev):
+    """The pointer of a reservation's status word, if there is one."""
+    if status is None:
+        return None
+    p = _tensor(status, "status", torch.int32, 1, dev)
+    if status.numel() != 1:
+        raise ValueError(f"status must have 1 entry, got {status.numel()}")
+    return p
+
+
+def _destination(k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, status, dev):
     """The checks fa_cache_append and fa_rope_append share: (k, v) rows and the pages' arguments."""
     pk, sk, T, Hkv, d = _rows(k, "k", _BF16, dev)
     pv, sv, Tv, Hv, dv = _rows(v, "v", _BF16, dev)
@@ -768,33 +781,37 @@ def _destination(k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale
     if ((Tv, Hv, dv) != (T, Hkv, d) or (H, dk) != (Hkv, d) or vpages.shape != kpages.shape or seqlens.numel() != B
             or cu_seqlens.numel() != B + 1):
         raise ValueError("shape mismatch between k, v, the pools, block_table, cu_seqlens and seqlens")
-    return (pk, sk), (pv, sv), (pkp, pvp, pks, pvs, pbt, pcu, psl), (T, B, Hkv, num_pages, page_size, max_pages, d)
+    return (pk, sk), (pv, sv), (pkp, pvp, pks, pvs, pbt, pcu, psl, _status(status, dev)), (T, B, Hkv, num_pages, page_size, max_pages, d)
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor,
                  block_table: torch.Tensor, cu_seqlens: torch.Tensor, seqlens: torch.Tensor,
-                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None, stream=None):
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None, stream=None,
+                 status: Optional[torch.Tensor] = None):
     """Put new tokens' k and v (T,Hkv,d), packed by cu_seqlens int32 (B+1,), into the pages
     (fa_cache_append): the last positions of sequences of length seqlens (which include them).
-    Pools (num_pages,Hkv,page_size,d) bf16, or uint8 E4M3 with k_scale / v_scale fp32 (Hkv,)."""
+    Pools (num_pages,Hkv,page_size,d) bf16, or uint8 E4M3 with k_scale / v_scale fp32 (Hkv,).
+    ``status`` is what pages_reserve wrote for these tokens: if it refused, nothing is written."""
     dev = _device_of(kpages, "kpages")
     (pk, sk), (pv, sv), ptrs, (T, B, Hkv, num_pages, page_size, max_pages, d) = _destination(
-        k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev)
+        k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, status, dev)
     if T == 0:
         return
-    _launch(load().fa_cache_append, dev, stream, pk, pv, *ptrs, T, B, Hkv, num_pages, page_size, max_pages, d, sk, sv)
+    _launch(load().fa_cache_append_ex, dev, stream, pk, pv, *ptrs, T, B, Hkv, num_pages, page_size, max_pages, d, sk, sv)
 
 
 def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
                 inv_freq: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor, block_table: torch.Tensor,
                 cu_seqlens: torch.Tensor, seqlens: torch.Tensor, axes: Optional[torch.Tensor] = None,
                 interleaved: bool = False, k_scale: Optional[torch.Tensor] = None,
-                v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
+                v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None,
+                status: Optional[torch.Tensor] = None):
     """rope of q and k and cache_append of the rotated k and of v in one launch
-    (fa_rope_append).  Returns q_out (None if q is None)."""
+    (fa_rope_append).  Returns q_out (None if q is None).  ``status`` as in cache_append; if the
+    reservation was refused, q_out is not written either."""
     dev = _device_of(kpages, "kpages")
     (pk, sk), (pv, sv), ptrs, (T, B, Hkv, num_pages, page_size, max_pages, d) = _destination(
-        k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, dev)
+        k, v, kpages, vpages, block_table, cu_seqlens, seqlens, k_scale, v_scale, status, dev)
     pq = po = None
     sq = so = Hq = 0
     if q is not None:
@@ -806,7 +823,7 @@ def rope_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pos
     pp, pf, pa, F, A = _rotation(positions, inv_freq, axes, T, dev)
     if T == 0:
         return q_out
-    _launch(load().fa_rope_append, dev, stream, pq, pk, pv, po, pp, pf, pa, *ptrs, T, B, Hq, Hkv, num_pages,
+    _launch(load().fa_rope_append_ex, dev, stream, pq, pk, pv, po, pp, pf, pa, *ptrs, T, B, Hq, Hkv, num_pages,
             page_size, max_pages, d, F, A, sq, sk, sv, so, 1 if interleaved else 0)
     return q_out
 
@@ -847,15 +864,18 @@ def pages_compact_workspace_size(num_pages: int) -> int:
 
 def pages_reserve(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, add: torch.Tensor,
                   page_size: int, copies: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                  stream=None) -> torch.Tensor:
+                  stream=None, status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Lengthen every slot s by add[s] tokens (fa_pages_reserve).  Returns copies int32 (S,2):
     {old, new} for each shared last page that was split, else -1; pass it to pages_copy for
-    every layer's pools.  Too few free pages: nothing changes, get_error() says so."""
+    every layer's pools.  Too few free pages: nothing changes; ``status`` int32 (1,) becomes
+    FA_ERR_NO_PAGES (FA_OK after a call that took place), or without it get_error() says so.
+    Tokens must not be appended after a refusal: pass the same ``status`` to rope_append or
+    cache_append, which then write nothing, or look first."""
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     pa = _list(add, "add", S, dev)
     pc, copies = _copies(copies, S, dev, stream)
     pw, nw, workspace = _scratch(workspace, pages_reserve_workspace_size, (S, num_pages), dev, stream)
-    _launch(load().fa_pages_reserve, dev, stream, *state, pa, pc, S, max_pages, num_pages, int(page_size), pw, nw)
+    _launch(load().fa_pages_reserve_ex, dev, stream, *state, pa, pc, _status(status, dev), S, max_pages, num_pages, int(page_size), pw, nw)
     return copies
 
 

@@ -356,6 +356,9 @@ FA_API int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const
  *             written and reported by fa_get_error (FA_ERR_DEVICE_ARG); rows from
  *             cu_seqlens[B] on (padding) are skipped.
  *   page_size a multiple of 16 (FA_ERR_UNSUPPORTED otherwise).
+ *   status (_ex; may be NULL): the word that fa_pages_reserve_ex wrote for these tokens.  Unless it
+ *             is FA_OK the lengths do not include them, and the positions above would be those of
+ *             finished tokens: the call then writes nothing at all.
  * Two tokens must not go to the same row of the same page (pages shared by several sequences
  * hold only finished positions; fa_pages_reserve sees to that).
  */
@@ -363,12 +366,17 @@ FA_API int fa_cache_append(const void *k, const void *v, void *kpages, void *vpa
                            const float *v_scale, const int *block_table, const int *cu_seqlens, const int *seqlens,
                            int T, int B, int Hkv, int num_pages, int page_size, int max_pages, int d,
                            long long k_stride, long long v_stride, void *stream);
+FA_API int fa_cache_append_ex(const void *k, const void *v, void *kpages, void *vpages, const float *k_scale,
+                              const float *v_scale, const int *block_table, const int *cu_seqlens,
+                              const int *seqlens, const int *status, int T, int B, int Hkv, int num_pages,
+                              int page_size, int max_pages, int d, long long k_stride, long long v_stride,
+                              void *stream);
 
 /*
  * fa_rope of q and k and fa_cache_append of the rotated k and of v in one launch: q_out gets
  * the rotated q (rows from cu_seqlens[B] on are left as they were), the pages get the rotated
  * keys (rounded once, to the cache's type) and the values.  Hq may be 0.  Arguments as in
- * those calls (bf16 q, k, v).
+ * those calls (bf16 q, k, v); with a status other than FA_OK q_out is left as it was, too.
  */
 FA_API int fa_rope_append(const void *q, const void *k, const void *v, void *q_out, const int *positions,
                           const float *inv_freq, const int *axes, void *kpages, void *vpages, const float *k_scale,
@@ -376,6 +384,13 @@ FA_API int fa_rope_append(const void *q, const void *k, const void *v, void *q_o
                           int T, int B, int Hq, int Hkv, int num_pages, int page_size, int max_pages, int d, int F,
                           int A, long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
                           int interleaved, void *stream);
+FA_API int fa_rope_append_ex(const void *q, const void *k, const void *v, void *q_out, const int *positions,
+                             const float *inv_freq, const int *axes, void *kpages, void *vpages,
+                             const float *k_scale, const float *v_scale, const int *block_table,
+                             const int *cu_seqlens, const int *seqlens, const int *status, int T, int B, int Hq,
+                             int Hkv, int num_pages, int page_size, int max_pages, int d, int F, int A,
+                             long long q_stride, long long k_stride, long long v_stride, long long q_out_stride,
+                             int interleaved, void *stream);
 
 /*
  * Page management.  The state is the caller's, in device memory:
@@ -397,6 +412,12 @@ FA_API int fa_rope_append(const void *q, const void *k, const void *v, void *q_o
  *   too few free pages (FA_ERR_NO_PAGES) or a slot that cannot grow so (FA_ERR_DEVICE_ARG)
  *   nothing changes and copies is all -1.  workspace: 16-byte aligned device scratch of
  *   fa_pages_reserve_workspace_size(S, num_pages) bytes; calls that share it must be ordered.
+ *   status (fa_pages_reserve_ex; int32 in device memory, may be NULL) is FA_OK after a call that
+ *   lengthened the slots, else the status above.  The caller's own record of a full pool, which is
+ *   no fault: with it FA_ERR_NO_PAGES stays out of the process-wide word that fa_get_error reads.
+ *   Tokens must not be appended after a call that refused (their positions would be those of
+ *   finished tokens): hand the same word to fa_cache_append_ex or fa_rope_append_ex, which then
+ *   write nothing, or ask fa_get_error before the append.
  * fa_pages_fork: for each of n pairs, the empty slot dst[i] becomes the first lengths[i]
  *   tokens of src[i] (lengths NULL: all); its pages are shared, no data moves.  A slot listed
  *   as a destination may not also be a source.  n <= 65535.
@@ -415,6 +436,9 @@ FA_API size_t fa_pages_reserve_workspace_size(int S, int num_pages);
 FA_API int fa_pages_reserve(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int S,
                             int max_pages, int num_pages, int page_size, void *workspace, size_t workspace_bytes,
                             void *stream);
+FA_API int fa_pages_reserve_ex(int *block_table, int *seqlens, int *refcount, const int *add, int *copies, int *status,
+                               int S, int max_pages, int num_pages, int page_size, void *workspace,
+                               size_t workspace_bytes, void *stream);
 FA_API int fa_pages_fork(int *block_table, int *seqlens, int *refcount, const int *src, const int *dst,
                          const int *lengths, int n, int S, int max_pages, int num_pages, int page_size, void *stream);
 FA_API int fa_pages_free(int *block_table, int *seqlens, int *refcount, const int *slots, const int *keep, int n,
