@@ -924,6 +924,33 @@ int launched(const char *what)
     return ok();
 }
 
+// What fa_get_error returns for the bits of the error word: one status a call, in this order.
+struct ErrorStatus {
+    unsigned int bits;
+    int status;
+};
+constexpr ErrorStatus kErrorStatuses[] = {
+    {fa::kErrTimeout, FA_ERR_TIMEOUT},
+    {fa::kErrSeqlenRange | fa::kErrPageRange | fa::kErrSlot | fa::kErrCuSeqlens | fa::kErrAxisRange, FA_ERR_DEVICE_ARG},
+    {fa::kErrNoPages, FA_ERR_NO_PAGES},
+    {fa::kErrDebugBounds, FA_ERR_DEBUG_CHECK},
+};
+
+struct ErrorMessage {
+    unsigned int bit;
+    const char *text;
+};
+constexpr ErrorMessage kErrorMessages[] = {
+    {fa::kErrTimeout, "a kernel pipeline wait exceeded its time limit"},
+    {fa::kErrSeqlenRange, "seqlens held a value outside [0, Nmax]"},
+    {fa::kErrPageRange, "the block table or a copy list held a page outside [0, num_pages)"},
+    {fa::kErrSlot, "page management: a slot, length or refcount was not usable"},
+    {fa::kErrCuSeqlens, "cu_seqlens does not ascend within [0, T], or disagrees with seqlens"},
+    {fa::kErrAxisRange, "axes held a value outside [0, A)"},
+    {fa::kErrNoPages, "the pool has fewer free pages than fa_pages_reserve needs; nothing was changed"},
+    {fa::kErrDebugBounds, "a kernel's global-memory index failed its bounds check (access skipped)"},
+};
+
 }  // namespace
 
 extern "C" {
@@ -1358,26 +1385,19 @@ int fa_get_error(void *stream)
 {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(FA_ERR_CUDA, "stream synchronize: %s", cudaGetErrorString(e));
-    unsigned int word = 0, zero = 0;
+    unsigned int word = 0;
     e = cudaMemcpyFromSymbol(&word, fa::g_error_word, sizeof word);
     if (e != cudaSuccess) return fail(FA_ERR_CUDA, "reading the error word: %s", cudaGetErrorString(e));
-    if (word) {
-        e = cudaMemcpyToSymbol(fa::g_error_word, &zero, sizeof zero);
+    for (const ErrorStatus &s : kErrorStatuses) {
+        if (!(word & s.bits)) continue;
+        cudaStream_t st = static_cast<cudaStream_t>(stream);
+        fa::fa_clear_errors_kernel<<<1, 1, 0, st>>>(s.bits & word);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaStreamSynchronize(st);
         if (e != cudaSuccess) return fail(FA_ERR_CUDA, "clearing the error word: %s", cudaGetErrorString(e));
+        for (const ErrorMessage &m : kErrorMessages)
+            if (word & s.bits & m.bit) return fail(s.status, "%s", m.text);
     }
-    if (word & fa::kErrTimeout) return fail(FA_ERR_TIMEOUT, "a kernel pipeline wait exceeded its time limit");
-    if (word & fa::kErrSeqlenRange) return fail(FA_ERR_DEVICE_ARG, "seqlens held a value outside [0, Nmax]");
-    if (word & fa::kErrPageRange)
-        return fail(FA_ERR_DEVICE_ARG, "the block table or a copy list held a page outside [0, num_pages)");
-    if (word & fa::kErrNoPages)
-        return fail(FA_ERR_NO_PAGES, "the pool has fewer free pages than fa_pages_reserve needs; nothing was changed");
-    if (word & fa::kErrSlot)
-        return fail(FA_ERR_DEVICE_ARG, "page management: a slot, length or refcount was not usable");
-    if (word & fa::kErrCuSeqlens)
-        return fail(FA_ERR_DEVICE_ARG, "cu_seqlens does not ascend within [0, T], or disagrees with seqlens");
-    if (word & fa::kErrAxisRange) return fail(FA_ERR_DEVICE_ARG, "axes held a value outside [0, A)");
-    if (word & fa::kErrDebugBounds)
-        return fail(FA_ERR_DEBUG_CHECK, "a kernel's global-memory index failed its bounds check (access skipped)");
     return ok();
 }
 

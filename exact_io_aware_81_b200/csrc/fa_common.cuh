@@ -24,6 +24,9 @@ __device__ unsigned int g_error_word = 0;
 
 __device__ __forceinline__ void raise_error(unsigned int bit) { atomicOr(&g_error_word, bit); }
 
+// Clears what the host has read, and only that: other bits may have been raised since.
+__global__ void fa_clear_errors_kernel(unsigned int bits) { atomicAnd(&g_error_word, ~bits); }
+
 // Debug builds (compiled with FA_DEBUG_CHECKS): every global-memory index that a kernel
 // computes by hand (outputs, partials, scales, block-table and q rows) is checked against
 // the size of its buffer before the access; a failed check records kErrDebugBounds and the

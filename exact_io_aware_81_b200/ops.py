@@ -941,7 +941,8 @@ def pages_copy(kpages: torch.Tensor, vpages: Optional[torch.Tensor], copies: tor
 
 
 def get_error(stream=None) -> int:
-    """Synchronise the stream and return (and clear) the device-side status."""
+    """Synchronise the stream and return (and clear) the device-side status; where several were
+    recorded, the next call returns the next."""
     return int(load().fa_get_error(_stream_handle(stream)))
 
 

@@ -450,9 +450,11 @@ FA_API int fa_pages_copy(void *kpages, void *vpages, const int *copies, int n, i
                          void *stream);
 
 /*
- * Synchronises `stream`, then reads and clears the device error word.  Returns FA_OK,
- * FA_ERR_TIMEOUT, FA_ERR_DEVICE_ARG, FA_ERR_NO_PAGES, FA_ERR_DEBUG_CHECK (debug builds), or
- * FA_ERR_CUDA if the synchronisation itself failed.
+ * Synchronises `stream`, then reads the device error word and clears what it returns of it:
+ * FA_ERR_TIMEOUT, FA_ERR_DEVICE_ARG, FA_ERR_NO_PAGES, FA_ERR_DEBUG_CHECK (debug builds), in this
+ * order, or FA_OK.  Where several were recorded the next call returns the next one.  FA_ERR_CUDA
+ * if the synchronisation itself failed.  There is one word per process: calls on any stream
+ * record in it, and whoever asks first is told.
  */
 FA_API int fa_get_error(void *stream);
 

@@ -138,3 +138,16 @@ def test_status_is_checked():
         with pytest.raises(ValueError):
             ops.cache_append(rows(1, 2, 128), rows(1, 2, 128), c.kp, c.vp, c.table, i32([0, 1, 1]), c.lens, status=bad)
     assert c.lens.tolist() == [20, 20]
+
+
+@pytest.mark.parametrize("other", ["page", "slot", "both"])
+def test_the_error_word_loses_nothing(other):
+    """A full pool and a bad argument in one step: fa_get_error returns one status after another."""
+    c = Cache()
+    ops.pages_reserve(*c.state, i32([1, 1]), PS)                  # too few pages
+    if other != "slot":
+        ops.pages_copy(c.kp, c.vp, i32([[0, 7]]))                 # no such page
+    if other != "page":
+        ops.pages_free(*c.state, i32([9]), PS)                    # no such slot
+    assert [ops.get_error() for _ in range(3)] == [ops.FA_ERR_DEVICE_ARG, ops.FA_ERR_NO_PAGES, ops.FA_OK]
+    assert c.lens.tolist() == [20, 20]
