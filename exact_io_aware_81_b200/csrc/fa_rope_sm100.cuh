@@ -90,16 +90,30 @@ __device__ __forceinline__ uint4 pack(const float (&f)[4], float)
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
 }
 
+// A scale as the two factors that values are multiplied by: `inv`, its reciprocal rounded to 24
+// bits, and `pre`, a power of two, other than 1 where 1 / scale is no normal number (below 2^-128
+// it would be infinite, and a zero NaN).  Both are always applied: a branch around the first took
+// 47 registers instead of 32, and the append of a prompt batch 22.6 us instead of 18.4.
+struct Scaling {
+    float pre, inv;
+};
+__device__ __forceinline__ Scaling scaling(float scale)
+{
+    const float a = fabsf(scale);
+    const float pre = a < 0x1p-126f ? 0x1p64f : a > 0x1p126f ? 0x1p-64f : 1.f;
+    return {pre, __frcp_rn(scale * pre)};
+}
+
 // Eight values times 1 / scale as E4M3 bytes, round to nearest even, saturated to +-448 (a NaN
 // stays one).  The reciprocal, rounded once per row to 32 bits, instead of a division per value:
 // the quotient is then off by at most 1.5 steps of 32 bits before it is rounded to 4 bits, and 16
 // divisions per thread and row made the append of a prompt batch 15% slower.
-__device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float inv_scale)
+__device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], const Scaling &s)
 {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * inv_scale, f[2 * i + 1] * inv_scale), __NV_SATFINITE,
+        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * i] * s.pre * s.inv, f[2 * i + 1] * s.pre * s.inv), __NV_SATFINITE,
                                         __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
@@ -322,10 +336,10 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
                 void *pool = is_k ? p.kpages : p.vpages;
                 if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
                 if constexpr (FP8) {
-                    const float inv_scale = __frcp_rn(is_k ? p.k_scale[h] : p.v_scale[h]);
+                    const Scaling sc = scaling(is_k ? p.k_scale[h] : p.v_scale[h]);
                     uint8_t *dst = static_cast<uint8_t *>(pool) + at;
-                    *reinterpret_cast<uint2 *>(dst + ca * V) = pack_e4m3(a, inv_scale);
-                    *reinterpret_cast<uint2 *>(dst + cb * V) = pack_e4m3(b, inv_scale);
+                    *reinterpret_cast<uint2 *>(dst + ca * V) = pack_e4m3(a, sc);
+                    *reinterpret_cast<uint2 *>(dst + cb * V) = pack_e4m3(b, sc);
                 } else {
                     T *dst = static_cast<T *>(pool) + at;
                     *reinterpret_cast<uint4 *>(dst + ca * V) = xa[u];
@@ -387,10 +401,10 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
                     if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
                     void *pool = is_k ? p.kpages : p.vpages;
                     if (FP8) {
-                        const float inv_scale = __frcp_rn(is_k ? p.k_scale[h] : p.v_scale[h]);
+                        const Scaling sc = scaling(is_k ? p.k_scale[h] : p.v_scale[h]);
                         uint8_t *dst = static_cast<uint8_t *>(pool) + at;
-                        dst[i0] = __nv_cvt_float_to_fp8(fx * inv_scale, __NV_SATFINITE, __NV_E4M3);
-                        dst[i1] = __nv_cvt_float_to_fp8(fy * inv_scale, __NV_SATFINITE, __NV_E4M3);
+                        dst[i0] = __nv_cvt_float_to_fp8(fx * sc.pre * sc.inv, __NV_SATFINITE, __NV_E4M3);
+                        dst[i1] = __nv_cvt_float_to_fp8(fy * sc.pre * sc.inv, __NV_SATFINITE, __NV_E4M3);
                     } else {
                         static_cast<T *>(pool)[at + i0] = x;
                         static_cast<T *>(pool)[at + i1] = y;

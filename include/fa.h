@@ -350,7 +350,8 @@ FA_API int fa_rope(const void *q, const void *k, void *q_out, void *k_out, const
  *   k, v      (T, Hkv, d) bf16, token strides k_stride / v_stride in elements
  *   kpages, vpages (num_pages, Hkv, page_size, d) bf16; with k_scale and v_scale (fp32 Hkv,
  *             both or neither) E4M3 bytes, byte = e4m3(value * (1 / scale[head])), the reciprocal
- *             rounded to fp32, the product rounded to nearest even and saturated; d = 128
+ *             rounded to 24 bits (in a range of its own: any scale but 0 has one), the product
+ *             rounded to nearest even and saturated; d = 128
  *   block_table int32 (B, max_pages), cu_seqlens int32 (B + 1) ascending from 0, seqlens
  *             int32 (B): device.  A token whose position or page does not exist is not
  *             written and reported by fa_get_error (FA_ERR_DEVICE_ARG); rows from
