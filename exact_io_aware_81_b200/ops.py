@@ -112,6 +112,13 @@ def status_str(status: int) -> str:
         return str(status)
 
 
+def _c_int(n) -> int:
+    """An integer of the caller's for a C int.  ctypes keeps the low 32 bits of a longer one, which
+    makes other numbers of them (a window of 2^32 + 5 one of 5); the nearest C int means the same
+    here: a window of all keys, or a size that the library refuses."""
+    return max(-2 ** 31, min(int(n), 2 ** 31 - 1))
+
+
 def _check(rc: int):
     if rc != FA_OK:
         raise FAError(rc, load().fa_last_error_message().decode())
@@ -206,7 +213,7 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
             raise ValueError("a sliding window needs causal=True")
         with _on_device(q, k, v, out, lse) as dev:
             rc = load().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                      lse.data_ptr(), B, Hq, Hkv, Nq, Nk, d, float(scale), int(window),
+                                      lse.data_ptr(), B, Hq, Hkv, Nq, Nk, d, float(scale), _c_int(window),
                                       odt, _stream_handle(stream, dev))
     else:
         with _on_device(q, k, v, out, lse) as dev:
@@ -246,7 +253,7 @@ def fwd_bshd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = F
     odt = FA_F32 if out_dtype == torch.float32 else FA_BF16
     with _on_device(q, k, v, out, lse) as dev:
         rc = load().fa_fwd_bshd(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                B, Hq, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), int(window), odt,
+                                B, Hq, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), _c_int(window), odt,
                                 _stream_handle(stream, dev))
     _check(rc)
     return out, lse
@@ -292,7 +299,7 @@ def fwd_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_scale: torch.Te
     with _on_device(q, k, v, q_scale, k_scale, v_scale, out, lse) as dev:
         rc = load().fa_fwd_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_scale.data_ptr(),
                                k_scale.data_ptr(), v_scale.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                               B, Hq, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), int(window), odt,
+                               B, Hq, Hkv, Nq, Nk, d, float(scale), int(bool(causal)), _c_int(window), odt,
                                _stream_handle(stream, dev))
     _check(rc)
     return out, lse
@@ -669,7 +676,7 @@ def fwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: 
         return out, lse
     pw, nw, workspace = _scratch(workspace, varlen_workspace_size, (B, Tq, Hq, Hkv), dev, stream)
     _launch(load().fa_fwd_varlen, dev, stream, pq, pk, pv, po, pl, pcq, pck, B, Tq, Tk, Hq, Hkv, d, sq, sk, sv,
-            float(scale), int(bool(causal)), int(window), odt, pw, nw)
+            float(scale), int(bool(causal)), _c_int(window), odt, pw, nw)
     return out, lse
 
 
@@ -699,7 +706,7 @@ def fwd_varlen_paged(q: torch.Tensor, kpages: torch.Tensor, vpages: torch.Tensor
         return out, lse
     pw, nw, workspace = _scratch(workspace, varlen_workspace_size, (B, Tq, Hq, Hkv), dev, stream)
     _launch(load().fa_fwd_varlen_paged, dev, stream, pq, pkp, pvp, pbt, pcq, psl, po, pl, B, Tq, Hq, Hkv, num_pages,
-            page_size, max_pages, d, sq, float(scale), int(bool(causal)), int(window), odt, pw, nw)
+            page_size, max_pages, d, sq, float(scale), int(bool(causal)), _c_int(window), odt, pw, nw)
     return out, lse
 
 
@@ -875,7 +882,7 @@ def pages_reserve(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
     pa = _list(add, "add", S, dev)
     pc, copies = _copies(copies, S, dev, stream)
     pw, nw, workspace = _scratch(workspace, pages_reserve_workspace_size, (S, num_pages), dev, stream)
-    _launch(load().fa_pages_reserve_ex, dev, stream, *state, pa, pc, _status(status, dev), S, max_pages, num_pages, int(page_size), pw, nw)
+    _launch(load().fa_pages_reserve_ex, dev, stream, *state, pa, pc, _status(status, dev), S, max_pages, num_pages, _c_int(page_size), pw, nw)
     return copies
 
 
@@ -890,7 +897,7 @@ def pages_fork(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch
     pl = _list(lengths, "lengths", n, dev) if lengths is not None else None
     if n == 0:
         return
-    _launch(load().fa_pages_fork, dev, stream, *state, ps, pd, pl, n, S, max_pages, num_pages, int(page_size))
+    _launch(load().fa_pages_fork, dev, stream, *state, ps, pd, pl, n, S, max_pages, num_pages, _c_int(page_size))
 
 
 def pages_free(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, slots: torch.Tensor,
@@ -903,7 +910,7 @@ def pages_free(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch
     pk = _list(keep, "keep", n, dev) if keep is not None else None
     if n == 0:
         return
-    _launch(load().fa_pages_free, dev, stream, *state, ps, pk, n, S, max_pages, num_pages, int(page_size))
+    _launch(load().fa_pages_free, dev, stream, *state, ps, pk, n, S, max_pages, num_pages, _c_int(page_size))
 
 
 def pages_compact(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: torch.Tensor, page_size: int,
@@ -914,7 +921,7 @@ def pages_compact(block_table: torch.Tensor, seqlens: torch.Tensor, refcount: to
     dev, state, (S, max_pages, num_pages) = _page_state(block_table, seqlens, refcount)
     pc, copies = _copies(copies, num_pages // 2, dev, stream)
     pw, nw, workspace = _scratch(workspace, pages_compact_workspace_size, (num_pages,), dev, stream)
-    _launch(load().fa_pages_compact, dev, stream, *state, pc, S, max_pages, num_pages, int(page_size), pw, nw)
+    _launch(load().fa_pages_compact, dev, stream, *state, pc, S, max_pages, num_pages, _c_int(page_size), pw, nw)
     return copies
 
 

@@ -65,6 +65,7 @@ def made(monkeypatch):
 
             def call(*a):
                 self.launched.append((name, a[-1]))
+                self.arguments = a
                 return ops.FA_OK
             return call
 
