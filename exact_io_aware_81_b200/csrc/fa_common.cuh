@@ -28,7 +28,7 @@ __device__ __forceinline__ void raise_error(unsigned int bit) { atomicOr(&g_erro
 __global__ void fa_clear_errors_kernel(unsigned int bits) { atomicAnd(&g_error_word, ~bits); }
 
 // Debug builds (compiled with FA_DEBUG_CHECKS): every global-memory index that a kernel
-// computes by hand (outputs, partials, scales, block-table and q rows) is checked against
+// computes by hand (outputs, partials, scales, q rows, page tables and lists) is checked against
 // the size of its buffer before the access; a failed check records kErrDebugBounds and the
 // access is skipped, so a bad index is reported instead of touching memory outside the
 // buffer.  (TMA copies are bounds-checked by the copy engine itself.)  In release builds the
@@ -45,6 +45,18 @@ __device__ __forceinline__ bool in_bounds(long long idx, long long n)
     if (idx >= 0 && idx < n) return true;
     raise_error(kErrDebugBounds);
     return false;
+}
+
+// Element i of a buffer of n elements, read and written behind that check.
+template <typename T>
+__device__ __forceinline__ T read_at(const T *p, long long i, long long n)
+{
+    return in_bounds(i, n) ? p[i] : T{};
+}
+template <typename T>
+__device__ __forceinline__ void write_at(T *p, long long i, long long n, const T &x)
+{
+    if (in_bounds(i, n)) p[i] = x;
 }
 
 // Per-CTA stop flag (in shared memory): set by the first role whose wait runs out, read

@@ -39,6 +39,23 @@ struct PageTables {
     int *seqlens;      // (S)
     int *refcount;     // (num_pages)
     int S, max_pages, num_pages, page_size;
+
+    __device__ __forceinline__ int length(int s) const { return read_at(seqlens, s, S); }
+    __device__ __forceinline__ void set_length(int s, int n) const { write_at(seqlens, s, S, n); }
+    __device__ __forceinline__ int page(int s, int j) const
+    {
+        return read_at(block_table, (long long)s * max_pages + j, (long long)S * max_pages);
+    }
+    __device__ __forceinline__ void set_page(int s, int j, int pg) const
+    {
+        write_at(block_table, (long long)s * max_pages + j, (long long)S * max_pages, pg);
+    }
+    __device__ __forceinline__ void set_count(int pg, int n) const { write_at(refcount, pg, num_pages, n); }
+    // adds to a page's count and returns what it was
+    __device__ __forceinline__ int count(int pg, int by) const
+    {
+        return in_bounds(pg, num_pages) ? atomicAdd(refcount + pg, by) : 0;
+    }
 };
 
 namespace pages {
@@ -87,11 +104,12 @@ __device__ __forceinline__ int block_scan(int v, int &total, int *warp_sums, int
 __device__ __forceinline__ int4 load4(const int *ref, int i, int n, int past)
 {
     int4 r = make_int4(past, past, past, past);
-    if (i + 3 < n && (reinterpret_cast<uintptr_t>(ref) & 15) == 0) return *reinterpret_cast<const int4 *>(ref + i);
-    if (i < n) r.x = ref[i];
-    if (i + 1 < n) r.y = ref[i + 1];
-    if (i + 2 < n) r.z = ref[i + 2];
-    if (i + 3 < n) r.w = ref[i + 3];
+    if (i + 3 < n && (reinterpret_cast<uintptr_t>(ref) & 15) == 0)
+        return in_bounds(i, n) ? *reinterpret_cast<const int4 *>(ref + i) : r;
+    if (i < n) r.x = read_at(ref, i, n);
+    if (i + 1 < n) r.y = read_at(ref, i + 1, n);
+    if (i + 2 < n) r.z = read_at(ref, i + 2, n);
+    if (i + 3 < n) r.w = read_at(ref, i + 3, n);
     return r;
 }
 
@@ -110,18 +128,18 @@ __global__ void __launch_bounds__(pages::kSlotThreads) fa_pages_fork_kernel(cons
 {
     using namespace pages;
     const int i = blockIdx.x;
-    const int s = p.src[i], d = p.dst[i];
+    const int s = read_at(p.src, i, p.n), d = read_at(p.dst, i, p.n);
     bool bad = s < 0 || s >= p.t.S || d < 0 || d >= p.t.S;
     for (int j = threadIdx.x; j < p.n; j += kSlotThreads) {
-        const int e = p.dst[j];
+        const int e = read_at(p.dst, j, p.n);
         bad |= e == s || (j < i && e == d);
     }
     int len = 0;
     if (!bad) {
-        len = p.t.seqlens[s];
-        bad = !len_ok(p.t, len) || p.t.seqlens[d] != 0;
+        len = p.t.length(s);
+        bad = !len_ok(p.t, len) || p.t.length(d) != 0;
         if (!bad && p.lengths) {
-            const int want = p.lengths[i];
+            const int want = read_at(p.lengths, i, p.n);
             bad = want < 0 || want > len;
             len = want;
         }
@@ -131,15 +149,13 @@ __global__ void __launch_bounds__(pages::kSlotThreads) fa_pages_fork_kernel(cons
         return;
     }
     const int np = pages_of(len, p.t.page_size);
-    const int *from = p.t.block_table + (long long)s * p.t.max_pages;
-    int *to = p.t.block_table + (long long)d * p.t.max_pages;
     for (int j = threadIdx.x; j < np; j += kSlotThreads) {
-        const int pg = from[j];
-        to[j] = pg;
-        if (pg >= 0 && pg < p.t.num_pages) atomicAdd(&p.t.refcount[pg], 1);
+        const int pg = p.t.page(s, j);
+        p.t.set_page(d, j, pg);
+        if (pg >= 0 && pg < p.t.num_pages) p.t.count(pg, 1);
         else raise_error(kErrPageRange);
     }
-    if (threadIdx.x == 0) p.t.seqlens[d] = len;
+    if (threadIdx.x == 0) p.t.set_length(d, len);
 }
 
 struct FreeParams {
@@ -153,16 +169,16 @@ __global__ void __launch_bounds__(pages::kSlotThreads) fa_pages_free_kernel(cons
 {
     using namespace pages;
     const int i = blockIdx.x;
-    const int s = p.slots[i];
+    const int s = read_at(p.slots, i, p.n);
     bool bad = s < 0 || s >= p.t.S;
-    for (int j = threadIdx.x; j < i; j += kSlotThreads) bad |= p.slots[j] == s;
+    for (int j = threadIdx.x; j < i; j += kSlotThreads) bad |= read_at(p.slots, j, p.n) == s;
     // every thread agrees on `bad` before the length is read: an earlier CTA of the same slot
     // may be writing it
     bool refused = __syncthreads_or(bad);
     int len = 0, keep = 0;
     if (!refused) {
-        len = p.t.seqlens[s];
-        if (p.keep) keep = p.keep[i];
+        len = p.t.length(s);
+        if (p.keep) keep = read_at(p.keep, i, p.n);
         refused = !len_ok(p.t, len) || keep < 0 || keep > len;
     }
     __syncthreads();  // the length is read by all before it changes
@@ -170,19 +186,18 @@ __global__ void __launch_bounds__(pages::kSlotThreads) fa_pages_free_kernel(cons
         if (threadIdx.x == 0) raise_error(kErrSlot);
         return;
     }
-    int *row = p.t.block_table + (long long)s * p.t.max_pages;
     const int end = pages_of(len, p.t.page_size);
     for (int j = pages_of(keep, p.t.page_size) + threadIdx.x; j < end; j += kSlotThreads) {
-        const int pg = row[j];
-        row[j] = -1;
+        const int pg = p.t.page(s, j);
+        p.t.set_page(s, j, -1);
         if (pg < 0 || pg >= p.t.num_pages) {
             raise_error(kErrPageRange);
-        } else if (atomicSub(&p.t.refcount[pg], 1) <= 0) {  // the page was not held
-            atomicAdd(&p.t.refcount[pg], 1);
+        } else if (p.t.count(pg, -1) <= 0) {  // the page was not held
+            p.t.count(pg, 1);
             raise_error(kErrSlot);
         }
     }
-    if (threadIdx.x == 0) p.t.seqlens[s] = keep;
+    if (threadIdx.x == 0) p.t.set_length(s, keep);
 }
 
 struct ReserveParams {
@@ -205,8 +220,8 @@ struct Need {
 __device__ __forceinline__ Need need_of(const ReserveParams &p, int s, bool &bad)
 {
     Need n;
-    const int add = p.add[s];
-    n.len = p.t.seqlens[s];
+    const int add = read_at(p.add, s, p.t.S);
+    n.len = p.t.length(s);
     n.begin = n.end = 0;
     n.split = -1;
     if (add == 0) return n;
@@ -217,10 +232,10 @@ __device__ __forceinline__ Need need_of(const ReserveParams &p, int s, bool &bad
     n.begin = pages_of(n.len, p.t.page_size);
     n.end = pages_of(n.len + add, p.t.page_size);
     if (n.len % p.t.page_size) {
-        const int last = p.t.block_table[(long long)s * p.t.max_pages + n.begin - 1];
+        const int last = p.t.page(s, n.begin - 1);
         if (last < 0 || last >= p.t.num_pages) {
             bad = true;
-        } else if (p.t.refcount[last] > 1) {
+        } else if (read_at(p.t.refcount, last, p.t.num_pages) > 1) {
             n.split = last;
             --n.begin;
         }
@@ -250,7 +265,7 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_reserve_kerne
         }
         int sum;
         const int at = block_scan(want, sum, warp_sums);
-        if (s < p.t.S) p.first[s] = total + at;
+        if (s < p.t.S) write_at(p.first, s, p.t.S, total + at);
         if (sum > p.t.num_pages - total) {
             total = p.t.num_pages + 1;
             break;
@@ -270,13 +285,13 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_reserve_kerne
             const int f0 = r.x <= 0, f1 = r.y <= 0, f2 = r.z <= 0, f3 = r.w <= 0;
             int sum;
             int at = found + block_scan(f0 + f1 + f2 + f3, sum, warp_sums);
-            if (f0 && at < total) p.free_ids[at] = i;
+            if (f0 && at < total) write_at(p.free_ids, at, p.t.num_pages, i);
             at += f0;
-            if (f1 && at < total) p.free_ids[at] = i + 1;
+            if (f1 && at < total) write_at(p.free_ids, at, p.t.num_pages, i + 1);
             at += f1;
-            if (f2 && at < total) p.free_ids[at] = i + 2;
+            if (f2 && at < total) write_at(p.free_ids, at, p.t.num_pages, i + 2);
             at += f2;
-            if (f3 && at < total) p.free_ids[at] = i + 3;
+            if (f3 && at < total) write_at(p.free_ids, at, p.t.num_pages, i + 3);
             found += sum;
         }
     }
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_reserve_kerne
             if (bad || !p.status) raise_error(bad ? kErrSlot : kErrNoPages);
             if (p.status) *p.status = bad ? FA_ERR_DEVICE_ARG : FA_ERR_NO_PAGES;
         }
-        for (int s = tid; s < 2 * p.t.S; s += kPlanThreads) p.copies[s] = -1;
+        for (int s = tid; s < 2 * p.t.S; s += kPlanThreads) write_at(p.copies, s, 2LL * p.t.S, -1);
         return;
     }
     if (p.status && tid == 0) *p.status = FA_OK;
@@ -299,30 +314,29 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_reserve_kerne
         Need n{0, 0, 0, -1};
         int at = 0, add = 0;
         if (s < p.t.S) {
-            add = p.add[s];
-            at = p.first[s];
+            add = read_at(p.add, s, p.t.S);
+            at = read_at(p.first, s, p.t.S);
             if (add > 0) {
-                n.len = p.t.seqlens[s];
+                n.len = p.t.length(s);
                 n.begin = pages_of(n.len, p.t.page_size);
                 n.end = pages_of(n.len + add, p.t.page_size);
-                const int next = s + 1 < p.t.S ? p.first[s + 1] : total;
+                const int next = s + 1 < p.t.S ? read_at(p.first, s + 1, p.t.S) : total;
                 if (next - at > n.end - n.begin) {
                     --n.begin;
-                    n.split = p.t.block_table[(long long)s * p.t.max_pages + n.begin];
+                    n.split = p.t.page(s, n.begin);
                 }
             }
         }
         const int want = n.end - n.begin;
         // short growth by the lane itself, longer growth by the whole warp
         constexpr int kOwn = 2;
-        int *row = p.t.block_table + (long long)(s < p.t.S ? s : 0) * p.t.max_pages;
         int split_to = -1;
 #pragma unroll
         for (int k = 0; k < kOwn; ++k) {
             if (k < want && (want <= kOwn || k == 0)) {
-                const int id = p.free_ids[at + k];
-                row[n.begin + k] = id;
-                p.t.refcount[id] = 1;
+                const int id = read_at(p.free_ids, at + k, p.t.num_pages);
+                p.t.set_page(s, n.begin + k, id);
+                p.t.set_count(id, 1);
                 if (k == 0) split_to = id;
             }
         }
@@ -332,18 +346,17 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_reserve_kerne
             more &= more - 1;
             const int ls = __shfl_sync(0xffffffffu, s, l), la = __shfl_sync(0xffffffffu, at, l);
             const int lb = __shfl_sync(0xffffffffu, n.begin, l), lw = __shfl_sync(0xffffffffu, want, l);
-            int *lrow = p.t.block_table + (long long)ls * p.t.max_pages;
             for (int k = 1 + lane; k < lw; k += 32) {
-                const int id = p.free_ids[la + k];
-                lrow[lb + k] = id;
-                p.t.refcount[id] = 1;
+                const int id = read_at(p.free_ids, la + k, p.t.num_pages);
+                p.t.set_page(ls, lb + k, id);
+                p.t.set_count(id, 1);
             }
         }
         if (s < p.t.S) {
-            if (add > 0) p.t.seqlens[s] = n.len + add;
-            if (n.split >= 0) atomicSub(&p.t.refcount[n.split], 1);
-            p.copies[2 * s] = n.split;
-            p.copies[2 * s + 1] = n.split >= 0 ? split_to : -1;
+            if (add > 0) p.t.set_length(s, n.len + add);
+            if (n.split >= 0) p.t.count(n.split, -1);
+            write_at(p.copies, 2 * s, 2LL * p.t.S, n.split);
+            write_at(p.copies, 2 * s + 1, 2LL * p.t.S, n.split >= 0 ? split_to : -1);
         }
     }
 }
@@ -380,10 +393,10 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_compact_kerne
         const int f0 = r.x <= 0, f1 = r.y <= 0, f2 = r.z <= 0, f3 = r.w <= 0;
         int sum;
         int at = holes + block_scan(f0 + f1 + f2 + f3, sum, warp_sums);
-        if (f0) p.holes[at++] = i;
-        if (f1) p.holes[at++] = i + 1;
-        if (f2) p.holes[at++] = i + 2;
-        if (f3) p.holes[at++] = i + 3;
+        if (f0) write_at(p.holes, at++, N, i);
+        if (f1) write_at(p.holes, at++, N, i + 1);
+        if (f2) write_at(p.holes, at++, N, i + 2);
+        if (f3) write_at(p.holes, at++, N, i + 3);
         holes += sum;
     }
     __syncthreads();  // the list of holes is complete
@@ -403,18 +416,21 @@ __global__ void __launch_bounds__(pages::kPlanThreads, 1) fa_pages_compact_kerne
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (ref[k] > 0 && i + k >= n_live) {
-                const int to = p.holes[at];
-                p.copies[2 * at] = i + k;
-                p.copies[2 * at + 1] = to;
-                p.rank[i + k] = at;
-                p.t.refcount[to] = ref[k];
-                p.t.refcount[i + k] = 0;
+                const int to = read_at(p.holes, at, N);
+                write_at(p.copies, 2 * at, N, i + k);
+                write_at(p.copies, 2 * at + 1, N, to);
+                write_at(p.rank, i + k, N, at);
+                p.t.set_count(to, ref[k]);
+                p.t.set_count(i + k, 0);
                 ++at;
             }
         }
         moved += sum;
     }
-    for (int k = moved + tid; k < N / 2; k += kPlanThreads) p.copies[2 * k] = p.copies[2 * k + 1] = -1;
+    for (int k = moved + tid; k < N / 2; k += kPlanThreads) {
+        write_at(p.copies, 2 * k, N, -1);
+        write_at(p.copies, 2 * k + 1, N, -1);
+    }
 }
 
 // The tables follow the pages: one CTA per slot.
@@ -423,21 +439,20 @@ __global__ void __launch_bounds__(pages::kSlotThreads) fa_pages_remap_kernel(con
     using namespace pages;
     const int s = blockIdx.x;
     const int n_live = *p.n_live;
-    const int len = p.t.seqlens[s];
+    const int len = p.t.length(s);
     if (!len_ok(p.t, len)) {
         if (threadIdx.x == 0) raise_error(kErrSlot);
         return;
     }
-    int *row = p.t.block_table + (long long)s * p.t.max_pages;
-    const int end = pages_of(len, p.t.page_size);
+    const int N = p.t.num_pages, end = pages_of(len, p.t.page_size);
     for (int j = threadIdx.x; j < end; j += kSlotThreads) {
-        const int pg = row[j];
+        const int pg = p.t.page(s, j);
         if (pg < 0 || pg >= p.t.num_pages) {
             raise_error(kErrPageRange);
         } else if (pg >= n_live) {
             // a page that did not move has no rank (it was not live): its line names another
-            const int k = p.rank[pg];
-            if (k >= 0 && k < p.t.num_pages / 2 && p.copies[2 * k] == pg) row[j] = p.copies[2 * k + 1];
+            const int k = read_at(p.rank, pg, N);
+            if (k >= 0 && k < N / 2 && read_at(p.copies, 2 * k, N) == pg) p.t.set_page(s, j, read_at(p.copies, 2 * k + 1, N));
             else raise_error(kErrSlot);
         }
     }
@@ -459,23 +474,25 @@ __global__ void __launch_bounds__(pages::kCopyThreads) fa_pages_copy_kernel(cons
     for (long long item = blockIdx.x; item < items; item += gridDim.x) {
         const long long e = item / per;
         const int c = (int)(item - e * per);
-        const int2 pair = make_int2(p.copies[2 * e], p.copies[2 * e + 1]);
+        const int2 pair = make_int2(read_at(p.copies, 2 * e, 2LL * p.n), read_at(p.copies, 2 * e + 1, 2LL * p.n));
         if (pair.x < 0 && pair.y < 0) continue;
         if (pair.x < 0 || pair.y < 0 || pair.x >= p.num_pages || pair.y >= p.num_pages) {
             if (threadIdx.x == 0) raise_error(kErrPageRange);
             continue;
         }
         uint4 *pool = c < p.pieces ? p.k : p.v;
+        const long long size = p.num_pages * p.page_vecs;
         const long long at = (long long)(c < p.pieces ? c : c - p.pieces) * (kCopyThreads * kCopyUnroll) + threadIdx.x;
-        const uint4 *src = pool + pair.x * p.page_vecs;
-        uint4 *dst = pool + pair.y * p.page_vecs;
+        const long long src = pair.x * p.page_vecs + at, dst = pair.y * p.page_vecs + at;
         uint4 x[kCopyUnroll];
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u)
-            if (at + u * kCopyThreads < p.page_vecs) x[u] = __ldcs(src + at + u * kCopyThreads);
+            if (at + u * kCopyThreads < p.page_vecs && in_bounds(src + u * kCopyThreads, size))
+                x[u] = __ldcs(pool + src + u * kCopyThreads);
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u)
-            if (at + u * kCopyThreads < p.page_vecs) __stcs(dst + at + u * kCopyThreads, x[u]);
+            if (at + u * kCopyThreads < p.page_vecs && in_bounds(dst + u * kCopyThreads, size))
+                __stcs(pool + dst + u * kCopyThreads, x[u]);
     }
 }
 

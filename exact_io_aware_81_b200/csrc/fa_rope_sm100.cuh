@@ -132,7 +132,7 @@ __device__ __forceinline__ void angle(int pos, float inv_freq, int inverse, floa
 __device__ __forceinline__ int axis_of(const RopeParams &p, int f)
 {
     if (!p.axes) return 0;
-    const int a = p.axes[f];
+    const int a = read_at(p.axes, f, p.F);
     if (a >= 0 && a < p.A) return a;
     raise_error(kErrAxisRange);
     return 0;
@@ -147,7 +147,7 @@ __device__ __forceinline__ int sequence_of(const int *cu, int B, int t)
     while (n > 0) {
         const int step = (n + 31) / 32;
         const int i = lo + (lane + 1) * step;  // entries up to i are <= t?
-        const bool le = (lane + 1) * step <= n && cu[i] <= t;
+        const bool le = (lane + 1) * step <= n && read_at(cu, i, B + 1) <= t;
         const int c = __popc(__ballot_sync(0xffffffffu, le));
         lo += c * step;
         n = min(step - 1, n - c * step);
@@ -167,18 +167,34 @@ __device__ __forceinline__ bool page_row_of(const RopeParams &p, int t, long lon
     row = -1;
     const int b = sequence_of(p.cu_seqlens, p.B, t);
     if (b >= p.B) return false;
-    const int c0 = p.cu_seqlens[b], n = p.cu_seqlens[b + 1] - c0;
-    const long long pos = (long long)p.seqlens[b] - n + (t - c0);
+    const int c0 = read_at(p.cu_seqlens, b, p.B + 1), n = read_at(p.cu_seqlens, b + 1, p.B + 1) - c0;
+    const long long pos = (long long)read_at(p.seqlens, b, p.B) - n + (t - c0);
     unsigned int err = 0;
     if (t < c0 || t - c0 >= n || pos < 0 || pos >= (long long)p.page_size * p.max_pages) {
         err = kErrCuSeqlens;
     } else {
-        const int pg = p.block_table[(long long)b * p.max_pages + pos / p.page_size];
+        const int pg = read_at(p.block_table, (long long)b * p.max_pages + pos / p.page_size, (long long)p.B * p.max_pages);
         if (pg < 0 || pg >= p.num_pages) err = kErrPageRange;
         else row = (long long)pg * p.Hkv * p.page_size + pos % p.page_size;
     }
     if (err && (threadIdx.x & 31) == 0) raise_error(err);
     return true;
+}
+
+// cos and sin of frequency f of token t.
+__device__ __forceinline__ void angle_of(const RopeParams &p, int f, int t, float &c, float &s)
+{
+    angle(read_at(p.positions, (long long)axis_of(p, f) * p.T + t, (long long)p.A * p.T), read_at(p.inv_freq, f, p.F),
+          p.inverse, c, s);
+}
+
+// Row h of token t in a (T, H, D) tensor with token stride s: a pointer to its elements, or null when
+// one of them would lie outside (debug builds; q, k, v and the outputs).
+template <int D, typename T>
+__device__ __forceinline__ T *row_at(const RopeParams &p, T *x, long long s, int H, long long t, int h)
+{
+    const long long at = t * s + (long long)h * D;
+    return in_bounds(at, (p.T - 1) * s + (long long)H * D - (D - 1)) ? x + at : nullptr;
 }
 
 }  // namespace rope
@@ -240,7 +256,7 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
         for (int i = tid; i < nt * p.F; i += kThreads) {
             const int t = i / p.F, f = i - t * p.F;
             float c, sn;
-            angle(p.positions[(long long)axis_of(p, f) * p.T + t0 + t], p.inv_freq[f], p.inverse, c, sn);
+            angle_of(p, f, t0 + t, c, sn);
             const int l = f / V, e = f % V;
             const int at = ((t * QV + e / 4) * LANES + l) * 4 + e % 4;
             ct[at] = c;
@@ -268,12 +284,14 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
             rows[u] = row;
             if (tok < nt) {
                 const long long t = t0 + tok;
-                const T *src = row < p.Hq           ? static_cast<const T *>(p.q) + t * p.q_s + (long long)row * D
-                               : row < p.Hq + p.Hkv ? static_cast<const T *>(p.k) + t * p.k_s + (long long)(row - p.Hq) * D
-                                                    : static_cast<const T *>(p.v) + t * p.v_s +
-                                                          (long long)(row - p.Hq - p.Hkv) * D;
-                xa[u] = *reinterpret_cast<const uint4 *>(src + ca * V);
-                xb[u] = *reinterpret_cast<const uint4 *>(src + cb * V);
+                const T *src = row < p.Hq ? row_at<D>(p, static_cast<const T *>(p.q), p.q_s, p.Hq, t, row)
+                               : row < p.Hq + p.Hkv
+                                   ? row_at<D>(p, static_cast<const T *>(p.k), p.k_s, p.Hkv, t, row - p.Hq)
+                                   : row_at<D>(p, static_cast<const T *>(p.v), p.v_s, p.Hkv, t, row - p.Hq - p.Hkv);
+                if (!kDebugChecks || src) {
+                    xa[u] = *reinterpret_cast<const uint4 *>(src + ca * V);
+                    xb[u] = *reinterpret_cast<const uint4 *>(src + cb * V);
+                }
             }
             row += hop;
             settle();
@@ -326,8 +344,9 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
                 if (rot_b) xb[u] = pack(b, T());
             }
             if (is_q || (is_k && !PAGES)) {
-                T *dst = is_q ? static_cast<T *>(p.q_out) + t * p.qo_s + (long long)r * D
-                              : static_cast<T *>(p.k_out) + t * p.ko_s + (long long)(r - p.Hq) * D;
+                T *dst = is_q ? row_at<D>(p, static_cast<T *>(p.q_out), p.qo_s, p.Hq, t, r)
+                              : row_at<D>(p, static_cast<T *>(p.k_out), p.ko_s, p.Hkv, t, r - p.Hq);
+                if (kDebugChecks && !dst) continue;
                 *reinterpret_cast<uint4 *>(dst + ca * V) = xa[u];
                 *reinterpret_cast<uint4 *>(dst + cb * V) = xb[u];
             } else if (PAGES && place >= 0) {
@@ -336,7 +355,7 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
                 void *pool = is_k ? p.kpages : p.vpages;
                 if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
                 if constexpr (FP8) {
-                    const Scaling sc = scaling(is_k ? p.k_scale[h] : p.v_scale[h]);
+                    const Scaling sc = scaling(read_at(is_k ? p.k_scale : p.v_scale, h, p.Hkv));
                     uint8_t *dst = static_cast<uint8_t *>(pool) + at;
                     *reinterpret_cast<uint2 *>(dst + ca * V) = pack_e4m3(a, sc);
                     *reinterpret_cast<uint2 *>(dst + cb * V) = pack_e4m3(b, sc);
@@ -371,7 +390,7 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
             const bool turned = f < p.F;
             int i0 = 2 * f, i1 = 2 * f + 1;
             if (turned) {
-                angle(p.positions[(long long)axis_of(p, f) * p.T + t], p.inv_freq[f], p.inverse, c, s);
+                angle_of(p, f, t, c, s);
                 if (!p.interleaved) {
                     i0 = f;
                     i1 = f + p.F;
@@ -380,10 +399,11 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
             for (int r = part; r < n_rows; r += p.split) {
                 const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv;
                 const int h = is_q ? r : is_k ? r - p.Hq : r - p.Hq - p.Hkv;
-                const T *src = is_q   ? static_cast<const T *>(p.q) + t * p.q_s
-                               : is_k ? static_cast<const T *>(p.k) + t * p.k_s
-                                      : static_cast<const T *>(p.v) + t * p.v_s;
-                T x = src[(long long)h * D + i0], y = src[(long long)h * D + i1];
+                const T *src = is_q   ? row_at<D>(p, static_cast<const T *>(p.q), p.q_s, p.Hq, t, h)
+                               : is_k ? row_at<D>(p, static_cast<const T *>(p.k), p.k_s, p.Hkv, t, h)
+                                      : row_at<D>(p, static_cast<const T *>(p.v), p.v_s, p.Hkv, t, h);
+                if (kDebugChecks && !src) continue;
+                T x = src[i0], y = src[i1];
                 float fx = (float)x, fy = (float)y;
                 if (turned && (is_q || is_k)) {
                     const float u = fx * c - fy * s, w = fx * s + fy * c;
@@ -393,15 +413,17 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
                     y = (T)w;
                 }
                 if (is_q || (is_k && !PAGES)) {
-                    T *dst = is_q ? static_cast<T *>(p.q_out) + t * p.qo_s : static_cast<T *>(p.k_out) + t * p.ko_s;
-                    dst[(long long)h * D + i0] = x;
-                    dst[(long long)h * D + i1] = y;
+                    T *dst = is_q ? row_at<D>(p, static_cast<T *>(p.q_out), p.qo_s, p.Hq, t, h)
+                                  : row_at<D>(p, static_cast<T *>(p.k_out), p.ko_s, p.Hkv, t, h);
+                    if (kDebugChecks && !dst) continue;
+                    dst[i0] = x;
+                    dst[i1] = y;
                 } else if (PAGES && page_row >= 0) {
                     const long long at = (page_row + (long long)h * p.page_size) * D;
                     if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
                     void *pool = is_k ? p.kpages : p.vpages;
                     if (FP8) {
-                        const Scaling sc = scaling(is_k ? p.k_scale[h] : p.v_scale[h]);
+                        const Scaling sc = scaling(read_at(is_k ? p.k_scale : p.v_scale, h, p.Hkv));
                         uint8_t *dst = static_cast<uint8_t *>(pool) + at;
                         dst[i0] = __nv_cvt_float_to_fp8(fx * sc.pre * sc.inv, __NV_SATFINITE, __NV_E4M3);
                         dst[i1] = __nv_cvt_float_to_fp8(fy * sc.pre * sc.inv, __NV_SATFINITE, __NV_E4M3);

@@ -79,17 +79,17 @@ struct Seq {
 __device__ __forceinline__ Seq sequence(const VarlenPlanParams &p, int b, bool &bad)
 {
     Seq s;
-    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+    const int q0 = read_at(p.cu_q, b, p.B + 1), q1 = read_at(p.cu_q, b + 1, p.B + 1);
     s.q0 = min(max(q0, 0), p.Tq);
     s.nq = min(max(q1, s.q0), p.Tq) - s.q0;
     bad |= s.q0 != q0 || s.q0 + s.nq != q1;
     if (p.seqlens) {
-        const int n = p.seqlens[b];
+        const int n = read_at(p.seqlens, b, p.B);
         s.k0 = 0;
         s.nk = min(max(n, 0), p.Tk);
         bad |= s.nk != n;
     } else {
-        const int k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+        const int k0 = read_at(p.cu_k, b, p.B + 1), k1 = read_at(p.cu_k, b + 1, p.B + 1);
         s.k0 = min(max(k0, 0), p.Tk);
         s.nk = min(max(k1, s.k0), p.Tk) - s.k0;
         bad |= s.k0 != k0 || s.k0 + s.nk != k1;
@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(varlen::kThreads, 1) fa_varlen_plan_kernel(con
     for (int j = tid; j < n_jobs; j += kThreads) {
         const int bin = job_of(j, s, b, r);
         const int to = atomicAdd(&bins[bin], 1);
-        p.plan[2 * to] = make_int4(s.q0, s.nq, s.k0, s.nk);
-        p.plan[2 * to + 1] = make_int4(r, b, 0, 0);
+        write_at(p.plan, 2 * to, 2LL * p.max_jobs, make_int4(s.q0, s.nq, s.k0, s.nk));
+        write_at(p.plan, 2 * to + 1, 2LL * p.max_jobs, make_int4(r, b, 0, 0));
     }
     if (tid == 0) {
         p.head[0] = n_jobs;
@@ -474,6 +474,11 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
         const int n_units = alone ? 0 : __ldcg(&p.plan_head[0]) * p.slots;
         const bool late = SHORT && n_units < 4 * (int)gridDim.x;
         auto draw = [&]() { return leader ? (int)gridDim.x + atomicAdd(&p.plan_head[1], 1) : 0; };
+        auto read_plan = [&](int job, int4 &x, int4 &y) {
+            if (!in_bounds(job, p.jobs.max_jobs)) return;
+            x = __ldcg(p.plan + 2 * job);
+            y = __ldcg(p.plan + 2 * job + 1);
+        };
         // A record's slot is reused four units later: Q(i) was issued, so unit i - 2 has released
         // its Q slots, and every role is done with unit i - 3, whose slot unit i + 1 takes.
         auto publish = [&](uint32_t i, bool valid, const Unit &uw) {
@@ -545,13 +550,12 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
         uint32_t i = 0;
         const int job0 = u / p.slots;
         slot = u - job0 * p.slots;
-        int4 x0, y0;
+        int4 x0 = make_int4(0, 0, 0, 0), y0 = x0;
         bool have;
         if (alone) {
             have = find_job(p.jobs, job0, x0, y0);
         } else if ((have = u < n_units)) {
-            x0 = __ldcg(&p.plan[2 * job0]);
-            y0 = __ldcg(&p.plan[2 * job0 + 1]);
+            read_plan(job0, x0, y0);
         }
         if (have) make_unit<WINDOW, SHORT>(p, x0, y0, slot, w);
         publish(0, have, w);
@@ -577,8 +581,7 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
                 if (have_n) {
                     const int job = u / p.slots;
                     slot = u - job * p.slots;
-                    px = __ldcg(&p.plan[2 * job]);
-                    py = __ldcg(&p.plan[2 * job + 1]);
+                    read_plan(job, px, py);
                     if (!late) next_raw = draw();
                 } else {
                     q_next = 2;

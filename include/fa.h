@@ -495,7 +495,7 @@ FA_API int fa_decode_selftest_timeout(const void *q, const void *kcache, const v
 /*
  * Build flags of this library: bit 0 set in the debug build (libfa_debug.so, compiled with
  * FA_DEBUG_CHECKS), whose kernels check every global-memory index they compute by hand
- * (outputs, decode partials, scales, q rows, block-table entries) against the size of its
+ * (outputs, decode partials, scales, q rows, page tables and lists) against the size of its
  * buffer, skip the access on a failure and report FA_ERR_DEBUG_CHECK through fa_get_error.
  * The results are the release build's; only speed differs.
  */
