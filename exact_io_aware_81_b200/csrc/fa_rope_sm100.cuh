@@ -188,13 +188,27 @@ __device__ __forceinline__ void angle_of(const RopeParams &p, int f, int t, floa
           p.inverse, c, s);
 }
 
-// Row h of token t in a (T, H, D) tensor with token stride s: a pointer to its elements, or null when
-// one of them would lie outside (debug builds; q, k, v and the outputs).
-template <int D, typename T>
-__device__ __forceinline__ T *row_at(const RopeParams &p, T *x, long long s, int H, long long t, int h)
+// Does row h of token t lie in a (T, H, D) tensor with token stride s (q, k, v and the outputs)?
+template <int D>
+__device__ __forceinline__ bool row_ok(const RopeParams &p, long long s, int H, long long t, int h)
 {
-    const long long at = t * s + (long long)h * D;
-    return in_bounds(at, (p.T - 1) * s + (long long)H * D - (D - 1)) ? x + at : nullptr;
+    return in_bounds(t * s + (long long)h * D, (p.T - 1) * s + (long long)H * D - (D - 1));
+}
+
+// The same for row r of the rows of token t that are read: those of q, then of k, then of v.
+template <int D>
+__device__ __forceinline__ bool source_ok(const RopeParams &p, long long t, int r)
+{
+    return r < p.Hq           ? row_ok<D>(p, p.q_s, p.Hq, t, r)
+           : r < p.Hq + p.Hkv ? row_ok<D>(p, p.k_s, p.Hkv, t, r - p.Hq)
+                              : row_ok<D>(p, p.v_s, p.Hkv, t, r - p.Hq - p.Hkv);
+}
+
+// And of the rows that are written to the outputs.
+template <int D>
+__device__ __forceinline__ bool output_ok(const RopeParams &p, long long t, int r)
+{
+    return r < p.Hq ? row_ok<D>(p, p.qo_s, p.Hq, t, r) : row_ok<D>(p, p.ko_s, p.Hkv, t, r - p.Hq);
 }
 
 }  // namespace rope
@@ -284,11 +298,11 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
             rows[u] = row;
             if (tok < nt) {
                 const long long t = t0 + tok;
-                const T *src = row < p.Hq ? row_at<D>(p, static_cast<const T *>(p.q), p.q_s, p.Hq, t, row)
-                               : row < p.Hq + p.Hkv
-                                   ? row_at<D>(p, static_cast<const T *>(p.k), p.k_s, p.Hkv, t, row - p.Hq)
-                                   : row_at<D>(p, static_cast<const T *>(p.v), p.v_s, p.Hkv, t, row - p.Hq - p.Hkv);
-                if (!kDebugChecks || src) {
+                const T *src = row < p.Hq           ? static_cast<const T *>(p.q) + t * p.q_s + (long long)row * D
+                               : row < p.Hq + p.Hkv ? static_cast<const T *>(p.k) + t * p.k_s + (long long)(row - p.Hq) * D
+                                                    : static_cast<const T *>(p.v) + t * p.v_s +
+                                                          (long long)(row - p.Hq - p.Hkv) * D;
+                if (source_ok<D>(p, t, row)) {
                     xa[u] = *reinterpret_cast<const uint4 *>(src + ca * V);
                     xb[u] = *reinterpret_cast<const uint4 *>(src + cb * V);
                 }
@@ -344,9 +358,9 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
                 if (rot_b) xb[u] = pack(b, T());
             }
             if (is_q || (is_k && !PAGES)) {
-                T *dst = is_q ? row_at<D>(p, static_cast<T *>(p.q_out), p.qo_s, p.Hq, t, r)
-                              : row_at<D>(p, static_cast<T *>(p.k_out), p.ko_s, p.Hkv, t, r - p.Hq);
-                if (kDebugChecks && !dst) continue;
+                T *dst = is_q ? static_cast<T *>(p.q_out) + t * p.qo_s + (long long)r * D
+                              : static_cast<T *>(p.k_out) + t * p.ko_s + (long long)(r - p.Hq) * D;
+                if (!output_ok<D>(p, t, r)) continue;
                 *reinterpret_cast<uint4 *>(dst + ca * V) = xa[u];
                 *reinterpret_cast<uint4 *>(dst + cb * V) = xb[u];
             } else if (PAGES && place >= 0) {
@@ -399,11 +413,11 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
             for (int r = part; r < n_rows; r += p.split) {
                 const bool is_q = r < p.Hq, is_k = !is_q && r < p.Hq + p.Hkv;
                 const int h = is_q ? r : is_k ? r - p.Hq : r - p.Hq - p.Hkv;
-                const T *src = is_q   ? row_at<D>(p, static_cast<const T *>(p.q), p.q_s, p.Hq, t, h)
-                               : is_k ? row_at<D>(p, static_cast<const T *>(p.k), p.k_s, p.Hkv, t, h)
-                                      : row_at<D>(p, static_cast<const T *>(p.v), p.v_s, p.Hkv, t, h);
-                if (kDebugChecks && !src) continue;
-                T x = src[i0], y = src[i1];
+                const T *src = is_q   ? static_cast<const T *>(p.q) + t * p.q_s
+                               : is_k ? static_cast<const T *>(p.k) + t * p.k_s
+                                      : static_cast<const T *>(p.v) + t * p.v_s;
+                if (!source_ok<D>(p, t, r)) continue;
+                T x = src[(long long)h * D + i0], y = src[(long long)h * D + i1];
                 float fx = (float)x, fy = (float)y;
                 if (turned && (is_q || is_k)) {
                     const float u = fx * c - fy * s, w = fx * s + fy * c;
@@ -413,11 +427,10 @@ __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const Ro
                     y = (T)w;
                 }
                 if (is_q || (is_k && !PAGES)) {
-                    T *dst = is_q ? row_at<D>(p, static_cast<T *>(p.q_out), p.qo_s, p.Hq, t, h)
-                                  : row_at<D>(p, static_cast<T *>(p.k_out), p.ko_s, p.Hkv, t, h);
-                    if (kDebugChecks && !dst) continue;
-                    dst[i0] = x;
-                    dst[i1] = y;
+                    T *dst = is_q ? static_cast<T *>(p.q_out) + t * p.qo_s : static_cast<T *>(p.k_out) + t * p.ko_s;
+                    if (!output_ok<D>(p, t, r)) continue;
+                    dst[(long long)h * D + i0] = x;
+                    dst[(long long)h * D + i1] = y;
                 } else if (PAGES && page_row >= 0) {
                     const long long at = (page_row + (long long)h * p.page_size) * D;
                     if (!in_bounds(at + D - 1, (long long)p.num_pages * p.Hkv * p.page_size * D)) continue;
