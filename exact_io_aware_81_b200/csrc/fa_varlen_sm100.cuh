@@ -620,8 +620,10 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
                     else if (SHORT && step == kLookUp) look_up();
                     else if (SHORT && step == kAsk && tiles - t <= 4) ask();
                 }
-                while (step == kTold && q_next < 2 &&
-                       __all_sync(0xffffffffu, ptx::mbar_test(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
+                // (a probe: a try_wait may suspend the warp until the slot is free, and K and V with it.
+                // With one set the slot is this unit's own, and not free before its end.)
+                while (C::kSets == 2 && step == kTold && q_next < 2 &&
+                       __all_sync(0xffffffffu, ptx::mbar_probe(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
                     issue_q(wn, i + 1, q_next);
                     ++q_next;
                 }

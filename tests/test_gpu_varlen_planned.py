@@ -305,3 +305,33 @@ def test_more_jobs_than_an_int_counts():
             ok[:n] |= (part[:n] == 0).all(-1)
             oz[:, :n] |= z[:, :n] == -math.inf
         assert ok.all() and oz.all()
+
+
+def test_short_units_cost_what_they_cost():
+    """Single tokens on contexts of 4096, SHORT, with just less and just more than four units a CTA
+    (where numbers are drawn late and early): a third more units may not take twice the time.  (While
+    the producer's look at the next unit's Q slot could suspend it, they took four times as long.)"""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Hq, Hkv, d, ps, ctx = 32, 8, 128, 64, 4096
+    times = {}
+    for B in (3 * sms // 8, -(-4 * sms // 8)):
+        mp = ctx // ps
+        assert variant_of(B, B, Hq, Hkv, B * ctx) == SHORT
+        kp, vp = (torch.randn(B * mp, Hkv, ps, d, device=DEV).to(torch.bfloat16) for _ in range(2))
+        table = torch.randperm(B * mp, device=DEV).to(torch.int32).view(B, mp)
+        q = torch.randn(B, Hq, d, device=DEV).to(torch.bfloat16)
+        cq, lens = torch.arange(B + 1, dtype=torch.int32, device=DEV), torch.full((B,), ctx, dtype=torch.int32, device=DEV)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        best = math.inf
+        for _ in range(6):
+            a.record()
+            o, lse = ops.fwd_varlen_paged(q, kp, vp, table, cq, lens)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times[B] = best
+        od, ld = ops.decode_paged(q, kp, vp, table, lens)
+        compare(o.cpu(), lse.cpu(), od.cpu().double(), ld.cpu().double().T, "against the decode kernel")
+    assert ops.get_error() == ops.FA_OK
+    few, many = times.values()
+    assert many < 2 * few, times
