@@ -735,17 +735,24 @@ int varlen_general(const void *q, const VarlenKeys &c, const int *cu_q, void *o,
     m.rows = 2 * p.tile_tokens;
     m.causal = p.causal;
     m.window = p.window;
-    // The variant for a few tokens against many keys -- many tiles without a partner, and units
-    // that are few and long -- judged by the averages, the lengths being known on the device only.
-    // Measured on B200 (32 + 8 heads, d = 128): 12 chunks of 1 to 512 tokens over contexts of up to
-    // 8192 165 us, 175 without it; 512 prompts of 64 tokens (no long context) 176 us against 163.
+    // SHORT is for a few tokens against many keys: tiles without a partner, units that are few and
+    // long.  The lengths are known on the device only, so the rule looks at what the host has: the
+    // tokens, the keys that k, or the pool and the table, can hold (a server's hold more than its
+    // sequences have), both on average, and how many units a CTA gets at most.  Measured on B200
+    // (32 + 8 heads, d = 128, pages of 64; us with SHORT / LONG): 12 chunks of 1 to 512 tokens over
+    // contexts of up to 8192 131 / 187, 24 such 124 / 158; single tokens on contexts of 4096 111 /
+    // 118 (37 of them) and 322 / 341 (111), of 1024 45 / 45 and 115 / 112, of 256 26 / 25 and 67 /
+    // 56; 512 prompts of 64 tokens with no context 211 / 157.  With many units there is little to
+    // gain, and up to a third to lose where the contexts are short: from five a CTA on it is LONG.
+    // (Calls of one wave run SHORT, without a plan, whatever this says.)
     const long long pool_keys = c.paged ? (long long)c.page_size * c.num_pages : keys;
     const long long all_keys = c.paged && pool_keys > keys * B ? keys * B : pool_keys;
-    const bool few = (long long)Tq <= 4LL * B * p.tile_tokens && all_keys >= 1024LL * B;
-    m.twins = few ? 1 : 0;
     m.max_jobs = varlen_max_jobs(B, Tq, pack);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const long long bound = (long long)m.max_jobs * slots;
+    const bool few = (long long)Tq <= 4LL * B * p.tile_tokens && all_keys >= 1024LL * B &&
+                     bound <= 5LL * info->num_sms;
+    m.twins = few ? 1 : 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool wave = bound <= info->num_sms;  // no more units than CTAs: no order to plan
     const int grid = wave ? (int)bound : info->num_sms;
     if (!wave) {

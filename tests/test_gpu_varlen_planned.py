@@ -1,7 +1,7 @@
 """Packed attention by the kernels that follow a plan: calls of more units than the GPU has SMs.
 
 Such a call runs the plan kernel and then one of two variants of the attention kernel, SHORT for a
-few tokens per sequence against long contexts, LONG otherwise; a call of fewer units runs SHORT
+few tokens per sequence against long contexts in few units, LONG otherwise; a call of fewer units runs SHORT
 without a plan (WAVE).  Every test here states the variant it is about and checks that its sizes
 choose it: the rule is restated below, and a call leaves its plan in the workspace.  All outputs are
 compared with the 64-bit restatement at the tolerances of the other attention calls."""
@@ -31,9 +31,10 @@ def variant_of(B, Tq, Hq, Hkv, all_keys):
     pack = pack_of(Hq // Hkv)
     tokens = 128 // pack
     bound = (Tq // (2 * tokens) + B) * (Hq // pack)
-    if bound <= torch.cuda.get_device_properties(0).multi_processor_count:
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    if bound <= sms:
         return WAVE
-    return SHORT if Tq <= 4 * B * tokens and all_keys >= 1024 * B else LONG
+    return SHORT if Tq <= 4 * B * tokens and all_keys >= 1024 * B and bound <= 5 * sms else LONG
 
 
 def units_of(nq, Hq, Hkv):
@@ -80,14 +81,14 @@ def lengths(kind, B, seed, most):
     return nq, nk
 
 
-# (kind, B, most tokens, Hq, Hkv, d): units per CTA from just over one to five, every pack form
+# (kind, B, most tokens, Hq, Hkv, d): units per CTA from just over one on, every pack form
 CASES = [
     (SHORT, 45, 90, 4, 4, 64),      # 180 units: numbers drawn late
     (SHORT, 45, 300, 4, 4, 128),    # pairs of tiles beside twins
     (SHORT, 80, 70, 8, 2, 128),
     (SHORT, 160, 30, 3, 1, 64),     # 126 rows a tile
-    (SHORT, 45, 90, 16, 16, 64),    # 704 units: more than four a CTA, numbers drawn early
-    (SHORT, 45, 40, 16, 16, 128),
+    (SHORT, 39, 90, 16, 16, 64),    # 608 units: more than four a CTA, numbers drawn early
+    (SHORT, 39, 40, 16, 16, 128),
     (LONG, 20, 300, 16, 16, 64),
     (LONG, 20, 300, 16, 16, 128),
     (LONG, 60, 200, 12, 4, 64),     # 126 rows a tile
@@ -305,6 +306,40 @@ def test_more_jobs_than_an_int_counts():
             ok[:n] |= (part[:n] == 0).all(-1)
             oz[:, :n] |= z[:, :n] == -math.inf
         assert ok.all() and oz.all()
+
+
+def test_many_units_are_long_whatever_the_pool_could_hold():
+    """512 short prompts whose table and pool could hold 8192 keys each: five units a CTA or more take
+    the LONG kernel (157 us where SHORT took 211)."""
+    from torch.profiler import ProfilerActivity, profile
+    B, nq, Hq, Hkv, d, ps, mp = 512, 64, 8, 2, 64, 64, 128
+    T = B * nq
+    g = torch.Generator().manual_seed(70)
+    q, k, v = make([T], [T], Hq, Hkv, d, 71)
+    pool = 17 * B   # 1088 keys a sequence
+    kp, vp = (torch.full((pool, Hkv, ps, d), math.nan, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pages = torch.randperm(pool, generator=g)[:B]
+    table = torch.full((B, mp), -1, dtype=torch.int32)
+    table[:, 0] = pages.to(torch.int32)
+    for p, x in ((kp, k), (vp, v)):
+        p[pages.to(DEV)] = x.to(DEV).view(B, ps, Hkv, d).transpose(1, 2)
+    n = cu([nq] * B)
+    assert variant_of(B, T, Hq, Hkv, ps * pool) == LONG
+    args = (q.to(DEV), kp, vp, table.to(DEV), n.to(DEV), torch.full((B,), nq, dtype=torch.int32, device=DEV))
+    o, lse = ops.fwd_varlen_paged(*args)
+    torch.cuda.synchronize()
+    with profile(activities=[ProfilerActivity.CUDA]) as prof:
+        o2, l2 = ops.fwd_varlen_paged(*args)
+        torch.cuda.synchronize()
+    assert ops.get_error() == ops.FA_OK and torch.equal(o, o2) and torch.equal(lse, l2)
+    some = [0, 1, 100, 511]
+    for b in some:
+        s = slice(b * nq, (b + 1) * nq)
+        ro, rl = serving.attention(q[s], k[s], v[s], d ** -0.5, True)
+        compare(o[s], lse[:, s], ro, rl, f"sequence {b}")
+    names = [m.group(1) for e in prof.key_averages() if (m := re.search(r"fa_varlen_kernel<([^>]*)>", e.key))]
+    if names:
+        assert len(names) == 1 and names[0].split(",")[-1].strip() in ("false", "0"), names
 
 
 def test_short_units_cost_what_they_cost():
