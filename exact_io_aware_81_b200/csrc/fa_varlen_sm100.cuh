@@ -620,10 +620,11 @@ __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(cons
                     else if (SHORT && step == kLookUp) look_up();
                     else if (SHORT && step == kAsk && tiles - t <= 4) ask();
                 }
-                // (a probe: a try_wait may suspend the warp until the slot is free, and K and V with it.
-                // With one set the slot is this unit's own, and not free before its end.)
+                // (With one set the slot is this unit's own: it is not free before the unit's end, and
+                // this look, a try_wait, would suspend the warp and with it K and V.  Of two sets the
+                // other is free within a tile or so; a plain probe there cost LONG 1%.)
                 while (C::kSets == 2 && step == kTold && q_next < 2 &&
-                       __all_sync(0xffffffffu, ptx::mbar_probe(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
+                       __all_sync(0xffffffffu, ptx::mbar_test(q_slot(i + 1, q_next), q_free_parity(i + 1)))) {
                     issue_q(wn, i + 1, q_next);
                     ++q_next;
                 }
