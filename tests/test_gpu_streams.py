@@ -131,3 +131,30 @@ def test_decode_workspace_and_outputs_on_a_busy_stream():
     intact = fill_like([ops.decode_workspace_size(B, Hq, N, d), 2 * B * Hq * d, 4 * B * Hq, wx.numel() * 2, wxl.numel() * 4])
     assert intact() and ops.get_error() == ops.FA_OK
     assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(xo, wx) and torch.equal(xl, wxl)
+
+
+def test_captured_on_a_forked_stream():
+    """Inside a capture: a side stream that joined it runs calls that make their outputs and their
+    workspace, some dropped at once."""
+    n, Hq, Hkv, d = [400, 129, 800, 33] * 8, 8, 2, 128
+    T = sum(n)
+    q, k, v = randn(T, Hq, d), randn(T, Hkv, d, seed=1), randn(T, Hkv, d, seed=2)
+    c, pos, inv = i32(np.cumsum([0] + n)), i32(np.arange(T)), torch.ones(64, device=DEV)
+    side = torch.cuda.Stream()
+    want, wl = ops.fwd_varlen(q, k, v, c, causal=True)
+    wq, wk = ops.rope(q, k, pos, inv)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        o = ops.fwd_varlen(q, k, v, c, causal=True, stream=side)[0]
+        lse = ops.fwd_varlen(q, k, v, c, causal=True, stream=side)[1]
+        qo, ko = ops.rope(q, k, pos, inv)
+        here.wait_stream(side)
+    for _ in range(3):
+        for t in (o, lse, qo, ko):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(qo, wq) and torch.equal(ko, wk)
+    assert ops.get_error() == ops.FA_OK
