@@ -16,7 +16,9 @@
 // tokens' sines and cosines once, into shared memory, then go over the rows, 2 x 16 bytes per
 // thread, the angles read back as needed, so few registers are held and many warps keep loads
 // in flight.  (16384 tokens of 32 + 8 heads, d = 128, bf16: 55.7 us = 6.0 TB/s, 0.92 of a plain
-// copy; a warp per token with the angles in registers, 105 of them, ran at 4.8 TB/s.)
+// copy; a warp per token with the angles in registers, 105 of them, ran at 4.8 TB/s.  12187 packed
+// tokens into pages: k and v alone 18.8 us as bf16 and 14.4 as E4M3, 0.81 and 0.79 of the copy rate;
+// with rotated k and q 54.2 and 58.8, 0.84 and 0.71.)
 //
 // PAGES: k and v rows go to row p % page_size of page block_table[b][p / page_size], p the
 // token's position in its sequence's cache, as bf16 or (FP8) as E4M3 bytes of the scaled value.
@@ -384,7 +386,8 @@ __global__ void __launch_bounds__(rope::kThreads) fa_rope_kernel(const RopeParam
 }
 
 // Any F: one lane per pair of one row, element by element; the copied elements follow.  Only
-// frequency counts that do not fill whole chunks come here.
+// frequency counts that do not fill whole chunks come here: bound by their 2- and 4-byte accesses
+// (16384 tokens of 32 + 8 heads, 13 frequencies, bf16: 157 us, where 64 take 55).
 template <int D, typename T, bool PAGES, bool FP8>
 __global__ void __launch_bounds__(32 * rope::kWarps) fa_rope_any_kernel(const RopeParams p)
 {

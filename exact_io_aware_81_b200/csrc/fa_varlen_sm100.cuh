@@ -21,6 +21,14 @@
 //     each unit to the other roles through a ring of records in shared memory.  A call whose
 //     units fit one wave of CTAs goes without a plan, each CTA finding its own (8 prompts of up
 //     to 64 tokens: 10.3 instead of 12.4 us).
+//   Rounding.  Scores, maxima, sums and the accumulators are 32 bits.  The weights are rounded to
+//     bf16, half a step of 2^-8 each, because the matrix instruction takes both operands in one
+//     type and V is bf16; the normaliser takes the rounding of a tile's largest weight back (see
+//     `lo`).  O is rounded once, to its type.  In relative norm the outputs are 0.0017-0.0023 from
+//     the 64-bit form; weights of 32 bits leave 0.0015-0.0017, the rounding of a bf16 O alone.
+//   Bits.  A unit's tiles, and with them the order of its sums, come from the lengths and the
+//     variant alone.  LONG and SHORT order them differently, so a sequence's last bits can change
+//     with what chooses the variant: the other lengths, the heads, and the size of the pool.
 //   Isolation.  A key tile that passes its sequence's end holds other rows (the next sequence's,
 //     or whatever a page has there): their scores are masked, and their V rows are cleared in
 //     shared memory before P V, since 0 * NaN would reach the output.
@@ -29,10 +37,12 @@
 //   Pages.  The producer's lanes look up the pages of a key tile's copies two tiles ahead and
 //     issue a copy each.
 // Bound: the softmax warps' latencies (a step, one key tile for both Q tiles, takes 1.75 us at
-// d = 64 and 128 alike; MUFU 44%, FMA 41%, tensor pipe 62% busy), and 3-4 us at each unit's
-// boundary.  Measured on B200, 32 + 8 heads, d = 128, causal: 9 sequences of 500 to 8192 tokens
-// 1.15-1.3 ms (1.05-1.2 PFLOP/s, with the clock); 16 prompts of 16 to 2048 tokens 98-109 us; 12
-// chunks of 1 to 512 tokens over paged contexts of up to 8192 tokens 145-160 us.
+// d = 64 and 128 alike; on 9 long sequences XU 46%, FMA 40%, tensor pipe 65% busy, with a window at
+// d = 64 25%, 25% and 18%), and 3-4 us at each unit's boundary.  Measured on B200, 32 + 8 heads,
+// d = 128, causal, replayed graphs, with the clock: 9 sequences of 500 to 8192 tokens 1.14-1.33 ms
+// (1.05-1.23 PFLOP/s), and four of 8192 1.91-2.03 ms, where the dense kernel takes 1.91-2.00; 16
+// prompts of 16 to 2048 tokens 96-106 us, up to 125 under the power cap; 12 chunks of 1 to 512 tokens
+// over paged contexts of up to 8192 tokens 131-137 us.
 #pragma once
 
 #include <cstdint>
@@ -244,8 +254,8 @@ struct Cfg {
     static constexpr int kTileBytes = 128 * D * 2;
     // Two sets of the unit's two Q tiles, so that the next unit's Q is loaded while one runs.  SHORT:
     // one set, and the room for more key tiles in flight -- units are few and long there, and every
-    // K/V tile is read by one CTA only, straight from HBM: twins took 3250 ns a pair of key tiles
-    // with 3 stages.
+    // K/V tile is read by one CTA only, straight from HBM: with two sets and 3 stages twins took 3.1
+    // us a pair of key tiles instead of 2.7, 12 paged chunks 164 us instead of 132.
     static constexpr int kSets = SHORT ? 1 : 2;
     static constexpr int kStages = (D == 128) ? (SHORT ? 5 : 3) : (SHORT ? 12 : 8);
     static constexpr int kQOff = 0;
@@ -353,9 +363,9 @@ __device__ __forceinline__ int warp_uniform(int v) { return __reduce_max_sync(0x
 
 // One persistent CTA per SM; roles by warp as in the prefill kernel (0-3 and 4-7 softmax of tiles
 // 0 and 1, 8 producer, 9 MMA, 10-11 idle).  SHORT: the variant for calls with few tokens per
-// sequence (see launch), with twins and late draws; their code in the other roles' way costs calls
-// without them 5% (measured on B200: four sequences of 8192 tokens 2136 against 2012 us), so
-// calls of long sequences get a kernel that has neither.
+// sequence in few units (see launch), with twins, late draws and one set of Q slots; all that costs
+// calls without twins 10% (measured on B200: four sequences of 8192 tokens 2.12 against 1.93 ms), so
+// calls of long sequences get a kernel that has none of it.
 template <int D, bool OUT_F32, bool WINDOW, bool PAGED, bool SHORT>
 __global__ void __launch_bounds__(varlen::kAttnThreads, 1) fa_varlen_kernel(const __grid_constant__ VarlenParams p)
 {

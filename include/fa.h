@@ -291,7 +291,9 @@ FA_API int fa_decode_noalloc(const void *q, const void *kcache, const void *vcac
  *             of n sees keys j <= i + (m - n) of m.  n > m is allowed here: a row that sees no
  *             key (also m = 0) gets o = 0, lse = -inf.  Sequences without rows are skipped.
  * Rows of o and lse that belong to no sequence are left as they were.  Nothing of one sequence
- * (NaN and infinities included) reaches another.
+ * (NaN and infinities included) reaches another.  The same call gives the same bits; the order in
+ * which a row's sums are taken, and so its last bits, can change with the other lengths, the heads
+ * and the size of a pool, which choose the kernel's variant.
  *   workspace: device scratch of fa_fwd_varlen_workspace_size(B, Tq, Hq, Hkv) bytes, 16-byte aligned,
  *             contents ignored and overwritten; calls that share it must be ordered.
  * Supported: d in {64, 128}, B <= 4096, Tq < 2^26, Tk < 2^30 (FA_ERR_UNSUPPORTED otherwise).
