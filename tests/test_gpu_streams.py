@@ -158,3 +158,69 @@ def test_captured_on_a_forked_stream():
         torch.cuda.synchronize()
         assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(qo, wq) and torch.equal(ko, wk)
     assert ops.get_error() == ops.FA_OK
+
+
+def planned_calls():
+    """Calls of more units than CTAs, both variants, each with a workspace of its own, and their results
+    one at a time: -> [(call(stream), wanted)]."""
+    Hq, Hkv, d, ps = 16, 8, 64, 64
+    calls = []
+    for seed, (B, most, ctx) in enumerate(((24, 60, 1500), (30, 300, 0), (28, 90, 1100), (40, 200, 60))):
+        r = np.random.RandomState(seed)
+        nq, cached = r.randint(1, most + 1, B), r.randint(0, 2 * ctx + 1, B) if ctx else np.zeros(B, int)
+        nk = nq + cached
+        T, need = int(nq.sum()), -(-nk // ps)
+        table = np.full((B, int(need.max())), -1, np.int32)
+        perm, at = r.permutation(int(need.sum())), 0
+        for b, m in enumerate(need):
+            table[b, :m] = perm[at:at + m]
+            at += m
+        q, kp, vp = randn(T, Hq, d, seed=seed), randn(at, Hkv, ps, d, seed=seed + 9), randn(at, Hkv, ps, d, seed=seed + 19)
+        args = (q, kp, vp, i32(table), i32(np.concatenate([[0], np.cumsum(nq)])), i32(nk))
+        ws = torch.full((ops.varlen_workspace_size(B, T, Hq, Hkv),), 0xFF, dtype=torch.uint8, device=DEV)
+        want = ops.fwd_varlen_paged(*args, workspace=ws)
+        assert int(ws[:4].view(torch.int32)) > 0, "not a planned call"
+        calls.append((lambda stream, args=args, ws=ws: ops.fwd_varlen_paged(*args, workspace=ws, stream=stream), want))
+    torch.cuda.synchronize()
+    return calls
+
+
+def test_planned_calls_on_streams_of_their_own():
+    calls = planned_calls()
+    streams = [torch.cuda.Stream() for _ in calls]
+    outs = []
+    for _ in range(20):
+        for (call, want), s in zip(calls, streams):
+            outs.append((call(s), want))
+    torch.cuda.synchronize()
+    assert ops.get_error() == ops.FA_OK
+    assert all(torch.equal(o, wo) and torch.equal(l, wl) for (o, l), (wo, wl) in outs)
+
+
+def test_calls_from_several_threads():
+    """One thread a stream, all in the library at once (the binding lets go of the interpreter there)."""
+    import threading
+    calls = planned_calls()
+    wrong = []
+
+    def work(call, want):
+        torch.cuda.set_device(0)
+        s = torch.cuda.Stream()
+        outs = [call(s) for _ in range(30)]
+        s.synchronize()
+        wrong.extend(1 for o, l in outs if not (torch.equal(o, want[0]) and torch.equal(l, want[1])))
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and ops.get_error() == ops.FA_OK
+
+
+def test_nothing_to_do_on_another_stream():
+    side = torch.cuda.Stream()
+    q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device=DEV)
+    o, lse = ops.fwd_varlen(q, q, q, i32([0, 0]), stream=side)
+    qo, _ = ops.rope(q, None, i32([]), torch.ones(32, device=DEV), stream=side)
+    assert o.shape == qo.shape == q.shape and tuple(lse.shape) == (4, 0) and ops.get_error() == ops.FA_OK
